@@ -56,7 +56,8 @@ typedef enum {
   HSQ_ERR_UNSUPPORTED = 3,   /* group not 64 or 128, r > 32, K or N not a multiple of 8 */
   HSQ_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed (launch, tensor map) */
   HSQ_ERR_TIMEOUT = 5,       /* a kernel gave up waiting (reported by hsq_get_device_status) */
-  HSQ_ERR_SCRATCH_LIMIT = 6  /* hsq_linear_forward_noalloc: shape needs more than HSQ_NOALLOC_SCRATCH_BYTES */
+  HSQ_ERR_SCRATCH_LIMIT = 6, /* hsq_linear_forward_noalloc: shape needs more than HSQ_NOALLOC_SCRATCH_BYTES */
+  HSQ_ERR_BAD_PAGE = 7       /* hsq_kv_append met a page outside its cache (reported by hsq_get_device_status) */
 } hsq_status;
 
 typedef enum { HSQ_OUT_BF16 = 0, HSQ_OUT_F32 = 1 } hsq_out_dtype;
@@ -280,6 +281,68 @@ hsq_status hsq_linear_forward_fused(const void* X_bf16, const float* s, const vo
                                     void* Y, hsq_out_dtype out, cudaStream_t stream);
 
 /*
+ * The forwards with an epilogue:
+ *   Y[m,n] = act(z[m,n]) * mul[m / mul_rows, n] + residual[m,n],
+ * z being what the forward of the same name without _ep computes (4-bit product
+ * + U L2 + bias), everything in fp32 with one rounding to the output type, so
+ * that a block's activation, gate and residual take no pass of their own.
+ *   act        none, relu, gelu (tanh form), gelu (erf form), silu
+ *   mul        NULL (none), or rows of N values, mul_ld elements apart; token m
+ *              takes row m / mul_rows: mul_rows = 1 for the other half of a gated
+ *              MLP, a sample's token count for its modulation gate
+ *   residual   NULL, or M rows of N values, residual_ld elements apart
+ * mul and residual are bf16 or fp32, each on its own.  They are 16-byte aligned,
+ * their row strides are multiples of 8 (HSQ_ERR_UNSUPPORTED otherwise) and at
+ * least N.  residual may be Y itself (the same pointer and type, stride N), and so
+ * may mul with mul_rows = 1; an operand that overlaps Y in any other way is
+ * refused (HSQ_ERR_INVALID_ARG).  A NULL epilogue, or one that asks for nothing,
+ * is the forward without it, bit for bit.
+ * The paper has no counterpart: in a transformer block these steps follow the
+ * linear's output elementwise.
+ *   hsq_linear_forward_ep        hsq_linear_forward, or hsq_linear_forward_pre
+ *                                where w_e4m3 is not NULL (workspace as for those)
+ *   hsq_linear_forward_x_ep      hsq_linear_forward_x
+ *   hsq_linear_forward_fused_ep  hsq_linear_forward_fused
+ *   hsq_fp4_linear_forward_ep    hsq_fp4_linear_forward (below)
+ */
+typedef enum {
+  HSQ_ACT_NONE = 0,
+  HSQ_ACT_RELU = 1,
+  HSQ_ACT_GELU_TANH = 2, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  HSQ_ACT_GELU_ERF = 3,  /* z/2 (1 + erf(z / sqrt 2)) */
+  HSQ_ACT_SILU = 4       /* z / (1 + e^-z) */
+} hsq_act;
+
+typedef struct {
+  hsq_act act;
+  const void* mul;
+  hsq_out_dtype mul_dtype;
+  int mul_rows;
+  long long mul_ld;
+  const void* residual;
+  hsq_out_dtype residual_dtype;
+  long long residual_ld;
+} hsq_epilogue;
+
+hsq_status hsq_linear_forward_ep(const uint8_t* x_codes, const float* x_scales, const float* U,
+                                 const uint8_t* w_codes, const float* w_scales, const uint8_t* w_e4m3,
+                                 const void* L2_bf16, const void* bias_bf16,
+                                 int M, int N, int K, int r, int group,
+                                 void* Y, hsq_out_dtype out, const hsq_epilogue* ep,
+                                 void* workspace, size_t ws_bytes, cudaStream_t stream);
+hsq_status hsq_linear_forward_x_ep(const void* X_bf16, const float* s, const void* L1_bf16,
+                                   const uint8_t* w_codes, const float* w_scales, const uint8_t* w_e4m3,
+                                   const void* L2_bf16, const void* bias_bf16,
+                                   int M, int N, int K, int r, int group,
+                                   void* Y, hsq_out_dtype out, const hsq_epilogue* ep,
+                                   void* workspace, size_t ws_bytes, cudaStream_t stream);
+hsq_status hsq_linear_forward_fused_ep(const void* X_bf16, const float* s, const void* L1_bf16,
+                                       const uint8_t* w_codes, const float* w_scales,
+                                       const void* L2_bf16, const void* bias_bf16,
+                                       int M, int N, int K, int r, int group,
+                                       void* Y, hsq_out_dtype out, const hsq_epilogue* ep, cudaStream_t stream);
+
+/*
  * The form hsq_linear_forward_fused takes for this shape on the current device:
  * 0 = none (the call returns HSQ_ERR_UNSUPPORTED, or INVALID_ARG for an invalid
  * shape), 1 = the weight stream, 2 = the cooperative decode tiles.  Host
@@ -362,6 +425,130 @@ hsq_status hsq_fp4_linear_forward(const uint8_t* x_codes, const uint8_t* x_sf, c
                                   const float* w_gs, const void* L2_bf16, const void* bias_bf16,
                                   int M, int N, int K, int r, void* Y, hsq_out_dtype out,
                                   cudaStream_t stream);
+hsq_status hsq_fp4_linear_forward_ep(const uint8_t* x_codes, const uint8_t* x_sf, const float* x_gs,
+                                     const float* U, const uint8_t* w_codes, const uint8_t* w_sf,
+                                     const float* w_gs, const void* L2_bf16, const void* bias_bf16,
+                                     int M, int N, int K, int r, void* Y, hsq_out_dtype out,
+                                     const hsq_epilogue* ep, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * At the output of a fused QKV linear: rotary positions, and the append of the
+ * new keys and values to a paged cache.  Both read the linear's output in place
+ * through strides (element (t, h, d) of a heads view is data[t * token_stride +
+ * h * head_stride + d]); the query and key heads of a fused output are
+ * neighbours, so one call rotates both.  The pages do not name these steps.
+ *
+ * Rotation: pair i of a head, at a token whose position along the pair's axis is
+ * p, turns by t = p * freqs[i]:
+ *     (x, y) -> scale * (x cos t - y sin t, x sin t + y cos t)
+ *   pairs        1 .. head_dim / 2 (head_dim <= 512); elements behind 2 * pairs
+ *                of a head pass through unchanged
+ *   interleaved  0: pair i joins elements i and pairs + i; else 2i and 2i + 1
+ *   pair_axis    host array [pairs]: the axis of each pair, below n_axes <=
+ *                HSQ_ROPE_MAX_AXES (time, height, width, ...); NULL for one axis
+ *   freqs        device fp32 [pairs], 4-byte aligned
+ *   transpose    nonzero turns by -t (scale unchanged): the gradient of the
+ *                rotation; with scale 1 also its inverse
+ *   scale        finite and not 0 (1 for a plain rotation)
+ * Angles are reduced in fp64, so they are good to fp32 for positions of any
+ * size that fp64 holds with its fraction of a turn to spare (|p f| < 10^8);
+ * products and sums are fp32, with one rounding to the output type.
+ *
+ * Pointers of these two calls need the alignment of their element type only;
+ * 16-byte aligned rows are faster.  Host structs are read during the call and may
+ * be reused afterwards.
+ */
+#define HSQ_ROPE_MAX_AXES 4
+
+typedef enum { HSQ_BF16 = 0, HSQ_F32 = 1, HSQ_E4M3 = 2 } hsq_dtype;
+typedef enum { HSQ_POS_I32 = 0, HSQ_POS_I64 = 1, HSQ_POS_F32 = 2 } hsq_pos_type;
+
+typedef struct {
+  void* data; /* only read where it is an input */
+  long long token_stride, head_stride;
+} hsq_heads;
+
+typedef struct {
+  const float* freqs;
+  const unsigned char* pair_axis;
+  int pairs, n_axes, interleaved, transpose;
+  float scale;
+} hsq_rotation;
+
+/* Positions [rows][n_axes], rows ld elements apart; token t reads row t % rows. */
+typedef struct {
+  const void* data;
+  hsq_pos_type type;
+  int rows;
+  long long ld;
+} hsq_positions;
+
+/*
+ * y = the rotation of x, [tokens][heads][head_dim] of dtype HSQ_BF16 or HSQ_F32.
+ * y may be x itself (the same view), or share no element with it (other overlaps
+ * are refused).  rows <= tokens: a batch whose samples share their positions
+ * passes one sample's rows.  tokens == 0 does nothing.
+ */
+hsq_status hsq_rope(const hsq_heads* x, const hsq_heads* y, hsq_dtype dtype, int tokens, int heads,
+                    int head_dim, const hsq_rotation* rot, const hsq_positions* pos, cudaStream_t stream);
+
+/*
+ * A paged cache: element (page, slot, head, d) of k is k[page * page_stride +
+ * slot * slot_stride + head * head_stride + d], the same strides for v.  The
+ * order of pages, slots and heads is free ([pages][page_size][kv_heads][D] or
+ * [pages][kv_heads][page_size][D], k and v apart or in one pool) as long as no two
+ * elements meet.  HSQ_E4M3 stores E4M3(x / scale[head]): fp32 division, nearest,
+ * ties to even, saturating at 448, NaN kept; k_scale and v_scale device fp32
+ * [kv_heads], all > 0, NULL for 1 and for the other types.
+ */
+typedef struct {
+  void *k, *v;
+  hsq_dtype dtype;
+  int pages, page_size;
+  long long page_stride, slot_stride, head_stride;
+  const float *k_scale, *v_scale;
+} hsq_paged_cache;
+
+/*
+ * The batch: sequence b owns tokens cu_seqlens[b] .. cu_seqlens[b+1] - 1 of the
+ * new ones (device int32 [count + 1], non-decreasing; an empty sequence is fine)
+ * and has cache_lens[b] tokens cached (device int32 [count], before this call;
+ * the call does not change it).  cu_seqlens NULL: one new token per sequence,
+ * count == tokens.  Cached token p of a sequence is slot p % page_size of page
+ * block_table[b][p / page_size] (device int32, max_pages entries a row, rows
+ * table_ld apart).
+ */
+typedef struct {
+  const int* block_table;
+  const int* cache_lens;
+  const int* cu_seqlens;
+  int count, max_pages;
+  long long table_ld;
+} hsq_sequences;
+
+/*
+ * Appends the new tokens' keys and values to the cache, rotating the keys, and
+ * rotates the queries on the way, in one launch.
+ *   k, v     [tokens][kv_heads][head_dim] of dtype HSQ_BF16 or HSQ_F32 (rounded
+ *            once to the cache's type)
+ *   q, q_out [tokens][q_heads][head_dim], both NULL iff q_heads == 0; q_out may be
+ *            q itself, or share no element with q, k and v
+ *   rot      NULL for no rotation (q is then copied)
+ *   pos      NULL: every axis takes the token's place in its sequence,
+ *            cache_lens[b] + t - cu_seqlens[b]; else positions of their own, rows ==
+ *            tokens (the slots still follow the places)
+ * Tokens in front of cu_seqlens[0] or from cu_seqlens[count] on (padding), and
+ * those of a sequence whose cache_lens is negative, are left alone: nothing is
+ * written for them.  Where a token's page is outside the cache, or its place
+ * behind max_pages, its k and v are not written and HSQ_ERR_BAD_PAGE is reported by
+ * hsq_get_device_status; the rest of the call is done.  No two tokens of a call
+ * may fall on one slot (which one it would hold is not defined).  The cache may not
+ * overlap q, k, v or q_out.  tokens == 0 does nothing.
+ */
+hsq_status hsq_kv_append(const hsq_heads* k, const hsq_heads* v, const hsq_heads* q, const hsq_heads* q_out,
+                         hsq_dtype dtype, int tokens, int q_heads, int kv_heads, int head_dim,
+                         const hsq_rotation* rot, const hsq_positions* pos, const hsq_paged_cache* cache,
+                         const hsq_sequences* seqs, cudaStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* hsq_status_string(hsq_status status);
@@ -369,7 +556,8 @@ const char* hsq_status_string(hsq_status status);
 /*
  * Synchronizes `stream`, then reads and clears the device status word of the
  * current device: HSQ_ERR_TIMEOUT if any kernel since the last read gave up
- * waiting, HSQ_ERR_CUDA if the synchronization itself failed, else HSQ_OK.
+ * waiting, else HSQ_ERR_BAD_PAGE if an hsq_kv_append met a page outside its cache,
+ * HSQ_ERR_CUDA if the synchronization itself failed, else HSQ_OK.
  */
 hsq_status hsq_get_device_status(cudaStream_t stream);
 

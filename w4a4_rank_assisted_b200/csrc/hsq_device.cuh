@@ -13,10 +13,12 @@
 
 namespace hsq {
 
-// Device status word (one per device): bit 0 = a wait timed out.
+// Device status word (one per device): bit 0 = a wait timed out, bit 1 = a cache
+// append met a page outside its cache.
 __device__ unsigned int g_status;
 
 constexpr unsigned kStatusTimeout = 1u;
+constexpr unsigned kStatusBadPage = 2u;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -24,6 +24,7 @@
 #pragma once
 
 #include "hsq_device.cuh"
+#include "hsq_epilogue.cuh"
 
 namespace hsq {
 
@@ -39,6 +40,8 @@ struct Fp4Args {
   int tiles_m, tiles_n;
   int out_f32;
   uint64_t limit_ns;
+  EpiArgs epi;  // kernels with EPI: act, mul and residual (hsq_epilogue.cuh)
+  void* Y;      // ... which write Y without the tensor map
 };
 
 // Tile 128 tokens x BN outputs; a stage is K = 256 (KCS = 4 chunks of K = 64).
@@ -82,7 +85,7 @@ struct Fp4Cfg {
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
-template <class Cfg>
+template <class Cfg, bool EPI = false>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                     const __grid_constant__ CUtensorMap tm_y, const Fp4Args args) {
@@ -292,6 +295,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
         }
         auto y = [&](int c) { return __uint_as_float(v[c >> 4][c & 15]); };
+        if constexpr (EPI) {
+          // 32 rows x 32 fp32 columns at a time through the staging buffer into row
+          // order, where mul and residual are read and Y is written
+#pragma unroll
+          for (int pz = 0; pz < 4; ++pz) {
+            EpiBox box;
+            epi_load_box(args.epi, y0, n0 + 32 * pz, args.M, args.N, box);
+            __syncwarp();  // the previous box has been read
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<float4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                  make_float4(y(32 * pz + 4 * c), y(32 * pz + 4 * c + 1), y(32 * pz + 4 * c + 2),
+                              y(32 * pz + 4 * c + 3));
+            __syncwarp();
+            epi_store_box(args.epi, stg, box, y0, n0 + 32 * pz, args.M, args.N, args.Y, args.out_f32);
+          }
+        } else
         // store: 32 rows x 128 bytes per TMA box, 128-byte swizzled staging
         if (!args.out_f32) {
 #pragma unroll

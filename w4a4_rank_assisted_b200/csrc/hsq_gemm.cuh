@@ -54,6 +54,7 @@
 #pragma once
 
 #include "hsq_device.cuh"
+#include "hsq_epilogue.cuh"
 #include "hsq_quant.cuh"
 
 #ifndef HSQ_ONE_PHASE
@@ -125,6 +126,7 @@ struct GemmArgs {
   float* fx_U;
   unsigned* fx_bar;
   int fx_zero_words;
+  EpiArgs epi;  // kernels with EPI: act, mul and residual (hsq_epilogue.cuh)
 };
 
 template <int BN_, int DH_, int STAGES_, bool SWAP_, int GPS_, int NI8_, int NTM_, int UNPACK_WARPS_ = 6,
@@ -228,6 +230,9 @@ struct GemmCfg {
   static_assert(!LR_MMA || PRE || (BM + BN) / 8 * LR_SBO <= I8_BYTES, "low-rank operands fit an int8 buffer");
   // with pre-expanded operands the low-rank operands get a buffer of their own
   static constexpr int LR_BYTES = (PRE && LR_MMA) ? (BM + B_ROWS) / 8 * LR_SBO : 0;
+  // Epilogue with act, mul and residual (GemmCfgEpi; instantiations of their own,
+  // so that the plain forwards keep their code unchanged)
+  static constexpr bool EPI = false;
   // Build the low-rank steps with build_lr_operands_mlp (the host takes these
   // kernels for ranks above LR_MAX_RANK; a separate instantiation, so that the
   // kernels for lower ranks keep their code unchanged)
@@ -270,6 +275,12 @@ struct GemmCfg {
   static_assert(32 * BPS <= 256, "TMA box width");
   static_assert(!PRE || GPS == 1, "pre-expanded operands: one group a stage");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
+// The same kernel with the epilogue of hsq_epilogue.cuh.
+template <class Base>
+struct GemmCfgEpi : Base {
+  static constexpr bool EPI = true;
 };
 
 // Unpack 16 packed bytes (32 codes) into two 16-byte int8 core-matrix rows
@@ -1340,7 +1351,34 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         if (lane == 0) *counter = 0u;
       }
       // the accumulators already hold U L2 + b (added by the tile's first unit)
-      if constexpr (Cfg::TMA_STORE) {
+      if constexpr (Cfg::TMA_STORE && Cfg::EPI) {
+        // The warp's 32 rows x 32 fp32 columns at a time go through its staging
+        // buffer (the fp32 layout below) into row order, where mul and residual
+        // are read and Y is written in whole 16-byte pieces; mul and residual are
+        // requested before the staging.
+        uint8_t* stg = ystage + dw * 4096;
+        const int y0 = tr * TILE_M + static_cast<int>(crank) * BM + q * 32;
+        const int x0 = tc * BN + h * CW;
+#pragma unroll
+        for (int pz = 0; pz < CW / 32; ++pz) {
+          EpiBox box;
+          epi_load_box(args.epi, y0, x0 + 32 * pz, args.M, args.N, box);
+          __syncwarp();  // the previous box has been read
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rl = qd + 8 * i;
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+              const int c16 = 2 * kb + (qc >> 1);
+              *reinterpret_cast<float2*>(stg + rl * 128 + ((c16 ^ (rl & 7)) << 4) + (qc & 1) * 8) =
+                  acc2[i * NBLK + 4 * pz + kb];
+            }
+          }
+          __syncwarp();
+          epi_store_box(args.epi, stg, box, y0, x0 + 32 * pz, args.M, args.N, args.Y, args.out_f32);
+        }
+        __syncwarp();
+      } else if constexpr (Cfg::TMA_STORE) {
         // Stage 32 rows x 128 bytes at a time in this warp's buffer, in the
         // 128-byte swizzled layout (16-byte chunk c of row r at chunk c ^ (r % 8),
         // so the quad-layout writes hit distinct banks), then one TMA store of
@@ -1415,13 +1453,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         for (int i = 0; i < 4; ++i) {
           const int n = rbase + 8 * i;
           if (n >= args.rows_r) continue;
+          float em[Cfg::EPI ? 2 * NBLK : 1], er[Cfg::EPI ? 2 * NBLK : 1];  // mul and residual, requested together
+          if constexpr (Cfg::EPI) {
+#pragma unroll
+            for (int t = 0; t < 2 * NBLK; ++t) {
+              const int m = col0 + 8 * (t >> 1) + (t & 1);
+              em[t] = m < args.M ? epi_mul_at(args.epi, m, n) : 0.f;
+              er[t] = m < args.M ? epi_res_at(args.epi, m, n) : 0.f;
+            }
+          }
 #pragma unroll
           for (int b = 0; b < NBLK; ++b) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int m = col0 + 8 * b + e;
               if (m < args.M) {
-                const float v = e ? acc2[i * NBLK + b].y : acc2[i * NBLK + b].x;
+                float v = e ? acc2[i * NBLK + b].y : acc2[i * NBLK + b].x;
+                if constexpr (Cfg::EPI) v = epi_value(args.epi, v, em[2 * b + e], er[2 * b + e]);
                 const size_t off = static_cast<size_t>(m) * args.N + n;
                 if (args.out_f32) static_cast<float*>(args.Y)[off] = v;
                 else static_cast<__nv_bfloat16*>(args.Y)[off] = __float2bfloat16_rn(v);

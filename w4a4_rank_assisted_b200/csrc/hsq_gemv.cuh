@@ -26,6 +26,7 @@
 #pragma once
 
 #include "hsq_device.cuh"
+#include "hsq_epilogue.cuh"
 #include "hsq_quant.cuh"
 
 namespace hsq {
@@ -51,6 +52,7 @@ struct GemvArgs {
   const float* s;           // [K]
   const __nv_bfloat16* L1;  // [K][r]
   int K, group;
+  EpiArgs epi;  // kernels with EPI: act, mul and residual (hsq_epilogue.cuh)
 };
 
 // Block: warp 0 streams the weights (one elected lane issues bulk copies),
@@ -130,8 +132,9 @@ __device__ __forceinline__ void gemv_compute_sync() { named_bar_sync(1, kGemvCom
 
 // MT: tokens the kernel is built for (M <= MT); LPG: lanes per scale group (a
 // lane holds 32 codes, so 2 for groups of 64 and 4 for groups of 128); RF: -1
-// reads the activation step's outputs, 0/1/2/4 is the fused form of that rank.
-template <int MT, int LPG, int RF = -1>
+// reads the activation step's outputs, 0/1/2/4 is the fused form of that rank;
+// EPI: with act, mul and residual.
+template <int MT, int LPG, int RF = -1, bool EPI = false>
 __global__ void __launch_bounds__(kGemvThreads, 1)
     w4a4_gemv_kernel(const __grid_constant__ CUtensorMap tm_sw, const GemvArgs a) {
   extern __shared__ __align__(16) uint8_t gemv_smem[];
@@ -321,6 +324,13 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
            i += kGemvComputeWarps) {
       const uint4* wrow = reinterpret_cast<const uint4*>(ring + (static_cast<size_t>(s) * a.rs + (i - it * a.rs)) * rowbytes);
       const int n = n0 + i;
+      float em = 1.f, er = 0.f;  // lane m: the row's mul and residual for token m, requested ahead of its sums
+      if constexpr (EPI) {
+        if (lane < a.M && lane < MT) {
+          em = epi_mul_at(a.epi, lane, n);
+          er = epi_res_at(a.epi, lane, n);
+        }
+      }
       float acc[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[m] = 0.f;
@@ -380,7 +390,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (lane == m && m < a.M) {
-          const float y = acc[m] + bn;
+          float y = acc[m] + bn;
+          if constexpr (EPI) y = epi_value(a.epi, y, em, er);
           const size_t off = static_cast<size_t>(m) * a.N + n;
           if (a.out_f32) static_cast<float*>(a.Y)[off] = y;
           else static_cast<__nv_bfloat16*>(a.Y)[off] = __float2bfloat16_rn(y);

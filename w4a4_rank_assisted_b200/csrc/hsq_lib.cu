@@ -2,7 +2,7 @@
 // validation, launch planning, tensor-map construction and kernel launches.
 //
 // Everything numeric happens in the kernels of hsq_quant.cuh, hsq_gemm.cuh,
-// hsq_gemv.cuh and hsq_lowrank.cuh (and, for the pack-time truncated-SVD
+// hsq_gemv.cuh, hsq_epilogue.cuh, hsq_rope.cuh and hsq_lowrank.cuh (and, for the pack-time truncated-SVD
 // helper only, plain fp32/fp64 cuBLAS GEMMs); this file checks arguments
 // (synchronously, before any launch), plans and launches.  It allocates no
 // device memory, except the helper's one cuBLAS handle per device.
@@ -10,18 +10,23 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <numeric>
 #include <utility>
 
 #include "../../include/hsq.h"
 #include "hsq_device.cuh"
+#include "hsq_epilogue.cuh"
 #include "hsq_fp4.cuh"
 #include "hsq_gemm.cuh"
 #include "hsq_gemv.cuh"
 #include "hsq_lowrank.cuh"
 #include "hsq_quant.cuh"
+#include "hsq_rope.cuh"
 
 namespace {
 
@@ -502,6 +507,60 @@ bool make_y_map(CUtensorMap* map, void* Y, int M, int N, bool f32) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// ------------------------------------------------------------------ epilogues
+// Whether the byte ranges [a, a + na) and [b, b + nb) meet.
+bool ranges_meet(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// Checks an epilogue for a Y of [M][N]: types, strides, alignment, and that an
+// operand that overlaps Y is Y itself, element for element (each element is then
+// read by the thread that writes it, before it does).  *ep becomes NULL where the
+// epilogue asks for nothing, so that the plain kernels serve the call.
+hsq_status check_epilogue(const hsq_epilogue** ep, int M, int N, const void* Y, hsq_out_dtype out) {
+  const hsq_epilogue* e = *ep;
+  if (!e) return HSQ_OK;
+  if (e->act < HSQ_ACT_NONE || e->act > HSQ_ACT_SILU) return HSQ_ERR_INVALID_ARG;
+  const size_t y_bytes = static_cast<size_t>(M) * N * (out == HSQ_OUT_F32 ? 4 : 2);
+  auto operand = [&](const void* p, hsq_out_dtype dt, int rows, long long ld, bool per_token) {
+    if (dt != HSQ_OUT_BF16 && dt != HSQ_OUT_F32) return HSQ_ERR_INVALID_ARG;
+    if (ld < N || ld > (1ll << 40)) return HSQ_ERR_INVALID_ARG;
+    if (ld % 8 != 0) return HSQ_ERR_UNSUPPORTED;
+    if (!aligned16(p)) return HSQ_ERR_ALIGNMENT;
+    const size_t es = dt == HSQ_OUT_F32 ? 4 : 2;
+    const size_t bytes = (static_cast<size_t>(rows - 1) * static_cast<size_t>(ld) + N) * es;
+    if (ranges_meet(p, bytes, Y, y_bytes) && !(p == Y && dt == out && per_token && (ld == N || M == 1)))
+      return HSQ_ERR_INVALID_ARG;
+    return HSQ_OK;
+  };
+  if (e->mul) {
+    if (e->mul_rows < 1) return HSQ_ERR_INVALID_ARG;
+    const int rows = (M - 1) / e->mul_rows + 1;
+    const hsq_status st = operand(e->mul, e->mul_dtype, rows, e->mul_ld, e->mul_rows == 1);
+    if (st != HSQ_OK) return st;
+  }
+  if (e->residual) {
+    const hsq_status st = operand(e->residual, e->residual_dtype, M, e->residual_ld, true);
+    if (st != HSQ_OK) return st;
+  }
+  if (e->act == HSQ_ACT_NONE && !e->mul && !e->residual) *ep = nullptr;
+  return HSQ_OK;
+}
+
+hsq::EpiArgs epi_args(const hsq_epilogue& e) {
+  hsq::EpiArgs a{};
+  a.act = static_cast<int>(e.act);
+  a.mul = e.mul;
+  a.mul_f32 = e.mul_dtype == HSQ_OUT_F32 ? 1 : 0;
+  a.mul_rows = e.mul ? e.mul_rows : 1;
+  a.mul_ld = e.mul_ld;
+  a.res = e.residual;
+  a.res_f32 = e.residual_dtype == HSQ_OUT_F32 ? 1 : 0;
+  a.res_ld = e.residual_ld;
+  return a;
+}
+
 template <class Cfg>
 hsq_status launch_gemm(const Plan& p, const CUtensorMap& tr, const CUtensorMap& tc, const CUtensorMap& ty,
                        const hsq::GemmArgs& a, cudaStream_t st) {
@@ -613,7 +672,7 @@ hsq_status launch_gemm_fused(const Plan& p, const CUtensorMap& tr, const CUtenso
 
 // `a` has the shape, rows_per_block and pointers set; the ring layout and the
 // wait limit are filled in here.
-template <int MT, int LPG, int RF = -1>
+template <int MT, int LPG, int RF = -1, bool EPI = false>
 hsq_status launch_gemv(const Plan& p, hsq::GemvArgs a, cudaStream_t st) {
   static std::mutex mu;
   static bool attr_set[64] = {false};
@@ -622,7 +681,7 @@ hsq_status launch_gemv(const Plan& p, hsq::GemvArgs a, cudaStream_t st) {
   {
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-      if (cudaFuncSetAttribute(hsq::w4a4_gemv_kernel<MT, LPG, RF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(hsq::w4a4_gemv_kernel<MT, LPG, RF, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(kGemvSmemMax)) != cudaSuccess)
         return HSQ_ERR_CUDA;
       if (dev >= 0 && dev < 64) attr_set[dev] = true;
@@ -637,7 +696,7 @@ hsq_status launch_gemv(const Plan& p, hsq::GemvArgs a, cudaStream_t st) {
   if (!make_scales_map(&tm_sw, a.w_scales, a.ldw, a.G, a.rows_per_block)) return HSQ_ERR_CUDA;
   // starts early: its weight copies do not depend on the preceding kernel, and
   // it waits for the activation step before reading its codes
-  if (launch_pdl(true, hsq::w4a4_gemv_kernel<MT, LPG, RF>, dim3(p.grid), dim3(hsq::kGemvThreads), L.bytes, st,
+  if (launch_pdl(true, hsq::w4a4_gemv_kernel<MT, LPG, RF, EPI>, dim3(p.grid), dim3(hsq::kGemvThreads), L.bytes, st,
                  tm_sw, a) != cudaSuccess)
     return HSQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? HSQ_OK : HSQ_ERR_CUDA;
@@ -683,6 +742,142 @@ struct BlasSlot {
   cublasHandle_t h = nullptr;
 };
 BlasSlot g_blas[kMaxDevices];
+
+// ------------------------------------------------------------------ rotary positions, cache append
+constexpr int kMaxHeadDim = 2 * hsq::kRopeMaxPairs;
+constexpr int kMaxHeads = 1 << 16;
+constexpr long long kMaxStride = 1ll << 40;
+
+size_t dtype_bytes(hsq_dtype t) { return t == HSQ_F32 ? 4 : t == HSQ_BF16 ? 2 : 1; }
+
+// Bytes of a heads view from its first element to its last.
+size_t view_bytes(const hsq_heads& v, int tokens, int heads, int dim, size_t es) {
+  return (static_cast<size_t>(tokens - 1) * v.token_stride + static_cast<size_t>(heads - 1) * v.head_stride + dim) * es;
+}
+
+hsq_status check_view(const hsq_heads* v, int tokens, int heads, int dim, size_t es, bool written) {
+  if (!v || !v->data) return HSQ_ERR_INVALID_ARG;
+  if (v->token_stride < 0 || v->head_stride < 0 || v->token_stride > kMaxStride || v->head_stride > kMaxStride)
+    return HSQ_ERR_INVALID_ARG;
+  if (v->token_stride > 0 && tokens - 1 > (1ll << 58) / v->token_stride) return HSQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(v->data) % es != 0) return HSQ_ERR_ALIGNMENT;
+  if (written) {
+    // the rows that are written are apart: heads inside tokens, or tokens inside heads
+    const long long hs = heads > 1 ? v->head_stride : kMaxStride, ts = tokens > 1 ? v->token_stride : kMaxStride;
+    if (hs < dim || ts < dim) return HSQ_ERR_INVALID_ARG;
+    if (heads > 1 && tokens > 1 && ts < (heads - 1) * hs + dim && hs < (tokens - 1) * ts + dim)
+      return HSQ_ERR_INVALID_ARG;
+  }
+  return HSQ_OK;
+}
+
+// Whether two heads views share no element: byte ranges apart, or column ranges
+// of the same rows (equal token strides, the spans of a token apart), or equal
+// stride patterns whose rows of `dim` fall on different residues.
+bool views_apart(const hsq_heads& a, int ha, const hsq_heads& b, int hb, int tokens, int dim, size_t es) {
+  if (!ranges_meet(a.data, view_bytes(a, tokens, ha, dim, es), b.data, view_bytes(b, tokens, hb, dim, es))) return true;
+  const long long diff = static_cast<long long>(reinterpret_cast<uintptr_t>(b.data)) -
+                         static_cast<long long>(reinterpret_cast<uintptr_t>(a.data));
+  auto apart_mod = [&](long long period, long long span_a, long long span_b) {
+    if (period <= 0) return false;
+    const long long p = period * static_cast<long long>(es), d = ((diff % p) + p) % p;
+    return span_a * static_cast<long long>(es) <= d && d + span_b * static_cast<long long>(es) <= p;
+  };
+  if (a.token_stride == b.token_stride &&
+      apart_mod(a.token_stride, (ha - 1) * a.head_stride + dim, (hb - 1) * b.head_stride + dim))
+    return true;
+  return apart_mod(std::gcd(std::gcd(a.token_stride, b.token_stride),
+                            std::gcd(ha > 1 ? a.head_stride : 0ll, hb > 1 ? b.head_stride : 0ll)),
+                   dim, dim);
+}
+
+hsq_status check_rotation(const hsq_rotation* r, int dim) {
+  if (!(std::fabs(r->scale) > 0.f) || std::isinf(r->scale)) return HSQ_ERR_INVALID_ARG;
+  if (!r->freqs || r->pairs < 1 || 2 * r->pairs > dim) return HSQ_ERR_INVALID_ARG;
+  if (r->n_axes < 1 || r->n_axes > HSQ_ROPE_MAX_AXES || (r->n_axes > 1 && !r->pair_axis)) return HSQ_ERR_INVALID_ARG;
+  if (r->pair_axis)
+    for (int i = 0; i < r->pairs; ++i)
+      if (r->pair_axis[i] >= r->n_axes) return HSQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(r->freqs) % 4 != 0) return HSQ_ERR_ALIGNMENT;
+  return HSQ_OK;
+}
+
+hsq_status check_positions(const hsq_positions* p, int n_axes, int max_rows) {
+  if (!p->data || p->rows < 1 || p->rows > max_rows) return HSQ_ERR_INVALID_ARG;
+  if (p->type != HSQ_POS_I32 && p->type != HSQ_POS_I64 && p->type != HSQ_POS_F32) return HSQ_ERR_INVALID_ARG;
+  if (p->ld < n_axes || p->ld > kMaxStride) return HSQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(p->data) % (p->type == HSQ_POS_I64 ? 8 : 4) != 0) return HSQ_ERR_ALIGNMENT;
+  return HSQ_OK;
+}
+
+hsq::RopeTable rope_table(const hsq_rotation* r, const hsq_positions* p) {
+  hsq::RopeTable t{};
+  t.pos_rows = 1;
+  if (!r) return t;
+  t.freqs = r->freqs;
+  t.pairs = r->pairs;
+  t.scale = r->scale;
+  t.sign = r->transpose ? -1.f : 1.f;
+  if (r->pair_axis)
+    for (int i = 0; i < r->pairs; ++i) t.axis2[i / 16] |= static_cast<uint32_t>(r->pair_axis[i]) << (2 * (i % 16));
+  if (p) {
+    t.pos = p->data;
+    t.pos_ld = p->ld;
+    t.pos_rows = p->rows;
+    t.pos_type = static_cast<int>(p->type);
+  }
+  return t;
+}
+
+// Base address and strides in bytes, or-ed: what has to be a multiple of a piece's bytes.
+uintptr_t view_bits(const hsq_heads& v, int tokens, int heads, size_t es) {
+  return reinterpret_cast<uintptr_t>(v.data) |
+         (static_cast<uintptr_t>((tokens > 1 ? v.token_stride : 0) | (heads > 1 ? v.head_stride : 0)) * es);
+}
+
+// The widest piece (elements) that a head's layout allows: 16 bytes of input, for
+// bf16 also 8 bytes, else single elements.  `bits`: view_bits of every tensor,
+// scaled to the input's element size.
+int piece_width(hsq_dtype t, int dim, int pairs, uintptr_t bits) {
+  const int es = static_cast<int>(dtype_bytes(t));
+  for (int v : {16 / es, 4}) {
+    if (pairs % v == 0 && (dim - 2 * pairs) % v == 0 && bits % (static_cast<uintptr_t>(v) * es) == 0) return v;
+  }
+  return 1;
+}
+
+// Threads that share the heads of a (token, unit): enough of them for about 1024
+// threads per SM, each with at least one head.
+void split_heads(long long tokens, int units, int heads, int& splits, int& per_split) {
+  const long long want = 1024ll * device_sm_count(), have = tokens * units;
+  long long s = (want + have - 1) / have;
+  s = std::max(1ll, std::min<long long>(s, heads));
+  per_split = static_cast<int>((heads + s - 1) / s);
+  splits = (heads + per_split - 1) / per_split;
+}
+
+template <typename T, int V>
+cudaError_t launch_rope(const hsq::RopeArgs& a, bool adjacent, cudaStream_t st) {
+  const long long n = static_cast<long long>(a.tokens) * a.splits * a.units;
+  const dim3 grid(static_cast<unsigned>((n + hsq::kRopeThreads - 1) / hsq::kRopeThreads));
+  return launch_pdl(true, adjacent ? hsq::rope_kernel<T, V, true> : hsq::rope_kernel<T, V, false>, grid,
+                    dim3(hsq::kRopeThreads), 0, st, a);
+}
+
+template <typename T, typename C, int V>
+cudaError_t launch_append(const hsq::AppendArgs& a, bool adjacent, cudaStream_t st) {
+  const long long n = static_cast<long long>(a.tokens) * a.splits * a.units;
+  const dim3 grid(static_cast<unsigned>((n + hsq::kRopeThreads - 1) / hsq::kRopeThreads));
+  return launch_pdl(true, adjacent ? hsq::kv_append_kernel<T, C, V, true> : hsq::kv_append_kernel<T, C, V, false>, grid,
+                    dim3(hsq::kRopeThreads), 0, st, a);
+}
+
+template <typename T, int V>
+cudaError_t launch_append(const hsq::AppendArgs& a, hsq_dtype cache, bool adjacent, cudaStream_t st) {
+  if (cache == HSQ_BF16) return launch_append<T, __nv_bfloat16, V>(a, adjacent, st);
+  if (cache == HSQ_F32) return launch_append<T, float, V>(a, adjacent, st);
+  return launch_append<T, uint8_t, V>(a, adjacent, st);
+}
 
 }  // namespace
 
@@ -756,7 +951,8 @@ int fused_form(int M, int N, int K, int r, int group, int nsm) {
 
 hsq_status forward_fused_dec16(const void* X_bf16, const float* s, const void* L1_bf16, const uint8_t* w_codes,
                                const float* w_scales, const void* L2_bf16, const void* bias_bf16, int M, int N, int K,
-                               int r, int group, void* Y, hsq_out_dtype out, cudaStream_t stream) {
+                               int r, int group, void* Y, hsq_out_dtype out, const hsq_epilogue* ep,
+                               cudaStream_t stream) {
   const int G = groups_of(K, group), Kp = G * group, nsm = device_sm_count();
   const FusedLayout FL = fused_dec16_layout(M, N, K, r, group, nsm);
   const Plan& p = FL.p;
@@ -798,6 +994,7 @@ hsq_status forward_fused_dec16(const void* X_bf16, const float* s, const void* L
   a.fx_upart = reinterpret_cast<float*>(base + o_up);
   a.fx_U = reinterpret_cast<float*>(base + o_u);
   a.fx_bar = reinterpret_cast<unsigned*>(base);
+  if (ep) a.epi = epi_args(*ep);
   a.lr_mma = 0;
   a.limit_ns = wait_limit_ns();
   if (t_debug_flags) {
@@ -805,6 +1002,9 @@ hsq_status forward_fused_dec16(const void* X_bf16, const float* s, const void* L
     a.limit_ns = static_cast<uint64_t>(t_debug_limit_ms > 0 ? t_debug_limit_ms : 50) * 1000000ull;
     t_debug_flags = 0;
   }
+  if (ep)
+    return group == 128 ? launch_gemm_fused<hsq::GemmCfgEpi<CfgDec16F_128>>(p, tm_row, tm_col, a, stream)
+                        : launch_gemm_fused<hsq::GemmCfgEpi<CfgDec16F_64>>(p, tm_row, tm_col, a, stream);
   return group == 128 ? launch_gemm_fused<CfgDec16F_128>(p, tm_row, tm_col, a, stream)
                       : launch_gemm_fused<CfgDec16F_64>(p, tm_row, tm_col, a, stream);
 }
@@ -928,6 +1128,7 @@ const char* hsq_status_string(hsq_status s) {
     case HSQ_ERR_CUDA: return "HSQ_ERR_CUDA";
     case HSQ_ERR_TIMEOUT: return "HSQ_ERR_TIMEOUT";
     case HSQ_ERR_SCRATCH_LIMIT: return "HSQ_ERR_SCRATCH_LIMIT";
+    case HSQ_ERR_BAD_PAGE: return "HSQ_ERR_BAD_PAGE";
   }
   return "HSQ_UNKNOWN_STATUS";
 }
@@ -944,7 +1145,7 @@ hsq_status hsq_get_device_status(cudaStream_t stream) {
   if (v) {
     const unsigned zero = 0;
     if (cudaMemcpyToSymbol(hsq::g_status, &zero, sizeof(zero)) != cudaSuccess) return HSQ_ERR_CUDA;
-    return HSQ_ERR_TIMEOUT;
+    return (v & hsq::kStatusTimeout) ? HSQ_ERR_TIMEOUT : HSQ_ERR_BAD_PAGE;
   }
   return HSQ_OK;
 }
@@ -1067,8 +1268,8 @@ static hsq_status quantize_act_impl(const void* X_bf16, const float* s, const vo
 static hsq_status forward_impl(const uint8_t* x_codes, const float* x_scales, const float* U, const uint8_t* w_codes,
                                const float* w_scales, const uint8_t* w_e4m3, const void* L2_bf16,
                                const void* bias_bf16, int M, int N, int K, int r, int group, void* Y,
-                               hsq_out_dtype out, void* workspace, size_t ws_bytes, cudaStream_t stream,
-                               bool x_expanded = false) {
+                               hsq_out_dtype out, const hsq_epilogue* ep, void* workspace, size_t ws_bytes,
+                               cudaStream_t stream, bool x_expanded = false) {
   hsq_status st = check_common(M, K, r, group);
   if (st != HSQ_OK) return st;
   if (N < 1 || N > kMaxDim) return HSQ_ERR_INVALID_ARG;
@@ -1081,6 +1282,8 @@ static hsq_status forward_impl(const uint8_t* x_codes, const float* x_scales, co
       (bias_bf16 && !aligned16(bias_bf16)) || (workspace && !aligned16(workspace)) ||
       (w_e4m3 && !aligned16(w_e4m3)))
     return HSQ_ERR_ALIGNMENT;
+  st = check_epilogue(&ep, M, N, Y, out);
+  if (st != HSQ_OK) return st;
 
   const int G = groups_of(K, group), Kp = G * group;
   const Plan p = make_plan(M, N, K, group, device_sm_count());
@@ -1101,6 +1304,13 @@ static hsq_status forward_impl(const uint8_t* x_codes, const float* x_scales, co
     ga.rows_per_block = p.tiles_r;
     const int mt = gemv_mt(M);
     const bool g128 = group == 128;
+    if (ep) {
+      ga.epi = epi_args(*ep);
+      if (mt == 1) return g128 ? launch_gemv<1, 4, -1, true>(p, ga, stream) : launch_gemv<1, 2, -1, true>(p, ga, stream);
+      if (mt == 2) return g128 ? launch_gemv<2, 4, -1, true>(p, ga, stream) : launch_gemv<2, 2, -1, true>(p, ga, stream);
+      if (mt == 4) return g128 ? launch_gemv<4, 4, -1, true>(p, ga, stream) : launch_gemv<4, 2, -1, true>(p, ga, stream);
+      return g128 ? launch_gemv<8, 4, -1, true>(p, ga, stream) : launch_gemv<8, 2, -1, true>(p, ga, stream);
+    }
     if (mt == 1) return g128 ? launch_gemv<1, 4>(p, ga, stream) : launch_gemv<1, 2>(p, ga, stream);
     if (mt == 2) return g128 ? launch_gemv<2, 4>(p, ga, stream) : launch_gemv<2, 2>(p, ga, stream);
     if (mt == 4) return g128 ? launch_gemv<4, 4>(p, ga, stream) : launch_gemv<4, 2>(p, ga, stream);
@@ -1172,26 +1382,20 @@ static hsq_status forward_impl(const uint8_t* x_codes, const float* x_scales, co
     t_debug_flags = 0;
   }
   const bool g128 = group == 128;
+  if (ep) a.epi = epi_args(*ep);
+#define HSQ_GEMM(CFG)                                                                  \
+  (ep ? launch_gemm<hsq::GemmCfgEpi<CFG>>(p, tm_row, tm_col, tm_y, a, stream)          \
+      : launch_gemm<CFG>(p, tm_row, tm_col, tm_y, a, stream))
   switch (p.kind) {
     case kLarge:
-      if (many_rank_kernel(r))
-        return g128 ? launch_gemm<CfgLarge128R>(p, tm_row, tm_col, tm_y, a, stream)
-                    : launch_gemm<CfgLarge64R>(p, tm_row, tm_col, tm_y, a, stream);
-      return g128 ? launch_gemm<CfgLarge128>(p, tm_row, tm_col, tm_y, a, stream)
-                  : launch_gemm<CfgLarge64>(p, tm_row, tm_col, tm_y, a, stream);
-    case kMid:
-      if (many_rank_kernel(r)) return launch_gemm<CfgMid64R>(p, tm_row, tm_col, tm_y, a, stream);
-      return launch_gemm<CfgMid64>(p, tm_row, tm_col, tm_y, a, stream);
-    case kDec16:
-      return g128 ? launch_gemm<CfgDec16_128>(p, tm_row, tm_col, tm_y, a, stream)
-                  : launch_gemm<CfgDec16_64>(p, tm_row, tm_col, tm_y, a, stream);
-    case kDec32:
-      return g128 ? launch_gemm<CfgDec32_128>(p, tm_row, tm_col, tm_y, a, stream)
-                  : launch_gemm<CfgDec32_64>(p, tm_row, tm_col, tm_y, a, stream);
-    case kDec64:
-      return g128 ? launch_gemm<CfgDec64_128>(p, tm_row, tm_col, tm_y, a, stream)
-                  : launch_gemm<CfgDec64_64>(p, tm_row, tm_col, tm_y, a, stream);
+      if (many_rank_kernel(r)) return g128 ? HSQ_GEMM(CfgLarge128R) : HSQ_GEMM(CfgLarge64R);
+      return g128 ? HSQ_GEMM(CfgLarge128) : HSQ_GEMM(CfgLarge64);
+    case kMid: return many_rank_kernel(r) ? HSQ_GEMM(CfgMid64R) : HSQ_GEMM(CfgMid64);
+    case kDec16: return g128 ? HSQ_GEMM(CfgDec16_128) : HSQ_GEMM(CfgDec16_64);
+    case kDec32: return g128 ? HSQ_GEMM(CfgDec32_128) : HSQ_GEMM(CfgDec32_64);
+    case kDec64: return g128 ? HSQ_GEMM(CfgDec64_128) : HSQ_GEMM(CfgDec64_64);
   }
+#undef HSQ_GEMM
   return HSQ_ERR_INVALID_ARG;
 }
 
@@ -1200,7 +1404,16 @@ hsq_status hsq_linear_forward(const uint8_t* x_codes, const float* x_scales, con
                               int r, int group, void* Y, hsq_out_dtype out, void* workspace, size_t ws_bytes,
                               cudaStream_t stream) {
   return forward_impl(x_codes, x_scales, U, w_codes, w_scales, nullptr, L2_bf16, bias_bf16, M, N, K, r, group, Y, out,
-                      workspace, ws_bytes, stream);
+                      nullptr, workspace, ws_bytes, stream);
+}
+
+hsq_status hsq_linear_forward_ep(const uint8_t* x_codes, const float* x_scales, const float* U, const uint8_t* w_codes,
+                                 const float* w_scales, const uint8_t* w_e4m3, const void* L2_bf16,
+                                 const void* bias_bf16, int M, int N, int K, int r, int group, void* Y,
+                                 hsq_out_dtype out, const hsq_epilogue* ep, void* workspace, size_t ws_bytes,
+                                 cudaStream_t stream) {
+  return forward_impl(x_codes, x_scales, U, w_codes, w_scales, w_e4m3, L2_bf16, bias_bf16, M, N, K, r, group, Y, out,
+                      ep, workspace, ws_bytes, stream);
 }
 
 hsq_status hsq_linear_forward_pre(const uint8_t* x_codes, const float* x_scales, const float* U,
@@ -1209,7 +1422,7 @@ hsq_status hsq_linear_forward_pre(const uint8_t* x_codes, const float* x_scales,
                                   void* Y, hsq_out_dtype out, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   if (!w_e4m3) return HSQ_ERR_INVALID_ARG;
   return forward_impl(x_codes, x_scales, U, w_codes, w_scales, w_e4m3, L2_bf16, bias_bf16, M, N, K, r, group, Y, out,
-                      workspace, ws_bytes, stream);
+                      nullptr, workspace, ws_bytes, stream);
 }
 
 // hsq_linear_forward_x's workspace: the GEMM's part first, then the activation
@@ -1247,6 +1460,15 @@ hsq_status hsq_linear_forward_x(const void* X_bf16, const float* s, const void* 
                                 const float* w_scales, const uint8_t* w_e4m3, const void* L2_bf16,
                                 const void* bias_bf16, int M, int N, int K, int r, int group, void* Y,
                                 hsq_out_dtype out, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  return hsq_linear_forward_x_ep(X_bf16, s, L1_bf16, w_codes, w_scales, w_e4m3, L2_bf16, bias_bf16, M, N, K, r, group,
+                                 Y, out, nullptr, workspace, ws_bytes, stream);
+}
+
+hsq_status hsq_linear_forward_x_ep(const void* X_bf16, const float* s, const void* L1_bf16, const uint8_t* w_codes,
+                                   const float* w_scales, const uint8_t* w_e4m3, const void* L2_bf16,
+                                   const void* bias_bf16, int M, int N, int K, int r, int group, void* Y,
+                                   hsq_out_dtype out, const hsq_epilogue* ep, void* workspace, size_t ws_bytes,
+                                   cudaStream_t stream) {
   hsq_status st = check_common(M, K, r, group);
   if (st != HSQ_OK) return st;
   if (N < 1 || N > kMaxDim) return HSQ_ERR_INVALID_ARG;
@@ -1258,6 +1480,8 @@ hsq_status hsq_linear_forward_x(const void* X_bf16, const float* s, const void* 
       !aligned16(workspace) || (w_e4m3 && !aligned16(w_e4m3)) || (L1_bf16 && !aligned16(L1_bf16)) ||
       (L2_bf16 && !aligned16(L2_bf16)) || (bias_bf16 && !aligned16(bias_bf16)))
     return HSQ_ERR_ALIGNMENT;
+  st = check_epilogue(&ep, M, N, Y, out);
+  if (st != HSQ_OK) return st;
   const int nsm = device_sm_count();
   const XLayout L = x_layout(M, N, K, r, group, nsm, w_e4m3 != nullptr);
   if (ws_bytes < L.total) return HSQ_ERR_INVALID_ARG;
@@ -1272,7 +1496,7 @@ hsq_status hsq_linear_forward_x(const void* X_bf16, const float* s, const void* 
     st = quantize_act_impl(X_bf16, s, L1_bf16, M, K, r, group, base + L.o_codes, xs, U, stream, zc, zc_words);
     if (st != HSQ_OK) return st;
     return forward_impl(base + L.o_codes, xs, U, w_codes, w_scales, w_e4m3, L2_bf16, bias_bf16, M, N, K, r, group,
-                        Y, out, workspace, L.gemm, stream);
+                        Y, out, ep, workspace, L.gemm, stream);
   }
   // the activation kernel writes the GEMM's E4M3 tiles (padding rows zeroed first)
   const int G = groups_of(K, group), Kp = G * group, ld = scales_ld(M);
@@ -1301,8 +1525,8 @@ hsq_status hsq_linear_forward_x(const void* X_bf16, const float* s, const void* 
   }
 #undef HSQ_X_ACT
   if (lerr != cudaSuccess || cudaGetLastError() != cudaSuccess) return HSQ_ERR_CUDA;
-  return forward_impl(xe, xs, U, w_codes, w_scales, w_e4m3, L2_bf16, bias_bf16, M, N, K, r, group, Y, out, workspace,
-                      L.gemm, stream, true);
+  return forward_impl(xe, xs, U, w_codes, w_scales, w_e4m3, L2_bf16, bias_bf16, M, N, K, r, group, Y, out, ep,
+                      workspace, L.gemm, stream, true);
 }
 
 size_t hsq_weights_e4m3_bytes(int N, int K, int group) {
@@ -1371,6 +1595,14 @@ hsq_status hsq_linear_forward_noalloc(const uint8_t* x_codes, const float* x_sca
 hsq_status hsq_linear_forward_fused(const void* X_bf16, const float* s, const void* L1_bf16, const uint8_t* w_codes,
                                     const float* w_scales, const void* L2_bf16, const void* bias_bf16, int M, int N,
                                     int K, int r, int group, void* Y, hsq_out_dtype out, cudaStream_t stream) {
+  return hsq_linear_forward_fused_ep(X_bf16, s, L1_bf16, w_codes, w_scales, L2_bf16, bias_bf16, M, N, K, r, group, Y,
+                                     out, nullptr, stream);
+}
+
+hsq_status hsq_linear_forward_fused_ep(const void* X_bf16, const float* s, const void* L1_bf16,
+                                       const uint8_t* w_codes, const float* w_scales, const void* L2_bf16,
+                                       const void* bias_bf16, int M, int N, int K, int r, int group, void* Y,
+                                       hsq_out_dtype out, const hsq_epilogue* ep, cudaStream_t stream) {
   hsq_status st = check_common(M, K, r, group);
   if (st != HSQ_OK) return st;
   if (N < 1 || N > kMaxDim) return HSQ_ERR_INVALID_ARG;
@@ -1389,9 +1621,11 @@ hsq_status hsq_linear_forward_fused(const void* X_bf16, const float* s, const vo
   // tokens: the decode tiles, the step spread over the grid
   const int form = fused_form(M, N, K, r, group, nsm);
   if (form == 0) return HSQ_ERR_UNSUPPORTED;
+  st = check_epilogue(&ep, M, N, Y, out);
+  if (st != HSQ_OK) return st;
   if (form == 2)
     return forward_fused_dec16(X_bf16, s, L1_bf16, w_codes, w_scales, L2_bf16, bias_bf16, M, N, K, r, group, Y, out,
-                               stream);
+                               ep, stream);
   Plan p{};
   p.kind = kGemv;
   p.tiles_r = gemv_rows_per_block(N, nsm);
@@ -1410,8 +1644,10 @@ hsq_status hsq_linear_forward_fused(const void* X_bf16, const float* s, const vo
   ga.L1 = static_cast<const __nv_bfloat16*>(L1_bf16);
   ga.K = K; ga.group = group;
   const bool g128 = group == 128;
-#define HSQ_FUSED(MTV, RV) \
-  return g128 ? launch_gemv<MTV, 4, RV>(p, ga, stream) : launch_gemv<MTV, 2, RV>(p, ga, stream)
+  if (ep) ga.epi = epi_args(*ep);
+#define HSQ_FUSED(MTV, RV)                                                                                        \
+  return ep ? (g128 ? launch_gemv<MTV, 4, RV, true>(p, ga, stream) : launch_gemv<MTV, 2, RV, true>(p, ga, stream)) \
+            : (g128 ? launch_gemv<MTV, 4, RV>(p, ga, stream) : launch_gemv<MTV, 2, RV>(p, ga, stream))
 #define HSQ_FUSED_R(MTV)          \
   switch (r) {                    \
     case 0: HSQ_FUSED(MTV, 0);    \
@@ -1427,6 +1663,168 @@ hsq_status hsq_linear_forward_fused(const void* X_bf16, const float* s, const vo
 }
 
 int hsq_fused_form(int M, int N, int K, int r, int group) { return fused_form(M, N, K, r, group, device_sm_count()); }
+
+// ------------------------------------------------------------------ rotary positions, cache append
+hsq_status hsq_rope(const hsq_heads* x, const hsq_heads* y, hsq_dtype dtype, int tokens, int heads, int head_dim,
+                    const hsq_rotation* rot, const hsq_positions* pos, cudaStream_t stream) {
+  if (dtype != HSQ_BF16 && dtype != HSQ_F32) return HSQ_ERR_INVALID_ARG;
+  if (tokens < 0 || heads < 1 || heads > kMaxHeads || head_dim < 2) return HSQ_ERR_INVALID_ARG;
+  if (head_dim > kMaxHeadDim) return HSQ_ERR_UNSUPPORTED;
+  if (!rot || !pos) return HSQ_ERR_INVALID_ARG;
+  hsq_status st = check_rotation(rot, head_dim);
+  if (st != HSQ_OK) return st;
+  if (tokens == 0) return HSQ_OK;
+  const size_t es = dtype_bytes(dtype);
+  if ((st = check_positions(pos, rot->n_axes, tokens)) != HSQ_OK) return st;
+  if ((st = check_view(x, tokens, heads, head_dim, es, false)) != HSQ_OK) return st;
+  if ((st = check_view(y, tokens, heads, head_dim, es, true)) != HSQ_OK) return st;
+  const bool in_place = x->data == y->data && (tokens == 1 || x->token_stride == y->token_stride) &&
+                        (heads == 1 || x->head_stride == y->head_stride);
+  if (!in_place && !views_apart(*x, heads, *y, heads, tokens, head_dim, es)) return HSQ_ERR_INVALID_ARG;
+  hsq::RopeArgs a{};
+  a.x = {x->data, x->token_stride, x->head_stride};
+  a.y = {y->data, y->token_stride, y->head_stride};
+  a.rot = rope_table(rot, pos);
+  a.tokens = tokens; a.heads = heads; a.dim = head_dim;
+  const uintptr_t bits = view_bits(*x, tokens, heads, es) | view_bits(*y, tokens, heads, es);
+  const int v = piece_width(dtype, head_dim, rot->pairs, bits);
+  a.units = rot->pairs / v + (in_place ? 0 : (head_dim - 2 * rot->pairs) / v);
+  split_heads(tokens, a.units, heads, a.splits, a.per_split);
+  if (static_cast<long long>(tokens) * a.splits * a.units > (1ll << 38)) return HSQ_ERR_UNSUPPORTED;
+  const bool adj = rot->interleaved != 0;
+  cudaError_t e;
+  if (dtype == HSQ_BF16)
+    e = v == 8 ? launch_rope<__nv_bfloat16, 8>(a, adj, stream)
+        : v == 4 ? launch_rope<__nv_bfloat16, 4>(a, adj, stream)
+                 : launch_rope<__nv_bfloat16, 1>(a, adj, stream);
+  else
+    e = v == 4 ? launch_rope<float, 4>(a, adj, stream) : launch_rope<float, 1>(a, adj, stream);
+  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? HSQ_OK : HSQ_ERR_CUDA;
+}
+
+hsq_status hsq_kv_append(const hsq_heads* k, const hsq_heads* v, const hsq_heads* q, const hsq_heads* q_out,
+                         hsq_dtype dtype, int tokens, int q_heads, int kv_heads, int head_dim,
+                         const hsq_rotation* rot, const hsq_positions* pos, const hsq_paged_cache* cache,
+                         const hsq_sequences* seqs, cudaStream_t stream) {
+  if (dtype != HSQ_BF16 && dtype != HSQ_F32) return HSQ_ERR_INVALID_ARG;
+  if (tokens < 0 || kv_heads < 1 || kv_heads > kMaxHeads || head_dim < 1) return HSQ_ERR_INVALID_ARG;
+  if (q_heads < 0 || q_heads > kMaxHeads || (q_heads > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr))
+    return HSQ_ERR_INVALID_ARG;
+  if (head_dim > kMaxHeadDim) return HSQ_ERR_UNSUPPORTED;
+  if (!cache || !seqs || (pos && !rot)) return HSQ_ERR_INVALID_ARG;
+  hsq_status st = HSQ_OK;
+  if (rot && (st = check_rotation(rot, head_dim)) != HSQ_OK) return st;
+  if (cache->dtype != HSQ_BF16 && cache->dtype != HSQ_F32 && cache->dtype != HSQ_E4M3) return HSQ_ERR_INVALID_ARG;
+  if (cache->dtype != HSQ_E4M3 && (cache->k_scale || cache->v_scale)) return HSQ_ERR_INVALID_ARG;
+  if (cache->pages < 1 || cache->page_size < 1 || seqs->count < 1 || seqs->max_pages < 1) return HSQ_ERR_INVALID_ARG;
+  if (tokens == 0) return HSQ_OK;
+  if (!cache->k || !cache->v || !seqs->block_table || !seqs->cache_lens) return HSQ_ERR_INVALID_ARG;
+  if (seqs->table_ld < seqs->max_pages || seqs->table_ld > kMaxStride) return HSQ_ERR_INVALID_ARG;
+  if (!seqs->cu_seqlens && seqs->count != tokens) return HSQ_ERR_INVALID_ARG;
+  const size_t es = dtype_bytes(dtype), cs = dtype_bytes(cache->dtype);
+  if ((st = check_view(k, tokens, kv_heads, head_dim, es, false)) != HSQ_OK) return st;
+  if ((st = check_view(v, tokens, kv_heads, head_dim, es, false)) != HSQ_OK) return st;
+  if (pos && ((st = check_positions(pos, rot->n_axes, tokens)) != HSQ_OK)) return st;
+  if (pos && pos->rows != tokens) return HSQ_ERR_INVALID_ARG;
+  bool in_place = false;
+  if (q) {
+    if ((st = check_view(q, tokens, q_heads, head_dim, es, false)) != HSQ_OK) return st;
+    if ((st = check_view(q_out, tokens, q_heads, head_dim, es, true)) != HSQ_OK) return st;
+    in_place = q->data == q_out->data && (tokens == 1 || q->token_stride == q_out->token_stride) &&
+               (q_heads == 1 || q->head_stride == q_out->head_stride);
+    if ((!in_place && !views_apart(*q, q_heads, *q_out, q_heads, tokens, head_dim, es)) ||
+        !views_apart(*k, kv_heads, *q_out, q_heads, tokens, head_dim, es) ||
+        !views_apart(*v, kv_heads, *q_out, q_heads, tokens, head_dim, es))
+      return HSQ_ERR_INVALID_ARG;
+  }
+  // the caches: strides of [pages][page_size][kv_heads][head_dim] in any order of
+  // the first three, rows apart, k and v apart from each other and from the inputs
+  size_t c_bytes = 0;
+  {
+    struct Dim { long long n, s; } d[3] = {{cache->pages, cache->page_stride},
+                                           {cache->page_size, cache->slot_stride},
+                                           {kv_heads, cache->head_stride}};
+    std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.s < b.s; });
+    long long extent = head_dim;  // elements from the first to the last so far
+    for (const Dim& x : d) {
+      if (x.s < 0 || x.s > kMaxStride) return HSQ_ERR_INVALID_ARG;
+      if (x.n == 1) continue;
+      if (x.s < extent) return HSQ_ERR_INVALID_ARG;
+      if (x.n - 1 > (1ll << 60) / x.s) return HSQ_ERR_INVALID_ARG;
+      extent += (x.n - 1) * x.s;
+      if (extent > (1ll << 60)) return HSQ_ERR_INVALID_ARG;
+    }
+    c_bytes = static_cast<size_t>(extent) * cs;
+  }
+  if (reinterpret_cast<uintptr_t>(cache->k) % cs || reinterpret_cast<uintptr_t>(cache->v) % cs ||
+      reinterpret_cast<uintptr_t>(seqs->block_table) % 4 || reinterpret_cast<uintptr_t>(seqs->cache_lens) % 4 ||
+      reinterpret_cast<uintptr_t>(seqs->cu_seqlens) % 4 || reinterpret_cast<uintptr_t>(cache->k_scale) % 4 ||
+      reinterpret_cast<uintptr_t>(cache->v_scale) % 4)
+    return HSQ_ERR_ALIGNMENT;
+  if (ranges_meet(cache->k, c_bytes, cache->v, c_bytes)) {
+    // k and v as halves of one pool: each other's rows on different residues of the page or slot stride
+    const long long diff = static_cast<long long>(reinterpret_cast<uintptr_t>(cache->v)) -
+                           static_cast<long long>(reinterpret_cast<uintptr_t>(cache->k));
+    auto apart = [&](long long period, long long span) {
+      const long long p = period * static_cast<long long>(cs), m = p > 0 ? ((diff % p) + p) % p : 0;
+      return span * static_cast<long long>(cs) <= m && m + span * static_cast<long long>(cs) <= p;
+    };
+    const long long ps = cache->pages > 1 ? cache->page_stride : 0, ss = cache->page_size > 1 ? cache->slot_stride : 0,
+                    hs = kv_heads > 1 ? cache->head_stride : 0;
+    const long long token = (kv_heads - 1) * hs + head_dim, page = (cache->page_size - 1) * ss + token;
+    if (!apart(ps, page) && !apart(std::gcd(ps, ss), token) && !apart(std::gcd(std::gcd(ps, ss), hs), head_dim))
+      return HSQ_ERR_INVALID_ARG;
+  }
+  const hsq_heads* in[4] = {k, v, q, q_out};
+  const int in_heads[4] = {kv_heads, kv_heads, q_heads, q_heads};
+  for (int i = 0; i < 4; ++i)
+    if (in[i])
+      for (const void* c : {cache->k, cache->v})
+        if (ranges_meet(in[i]->data, view_bytes(*in[i], tokens, in_heads[i], head_dim, es), c, c_bytes))
+          return HSQ_ERR_INVALID_ARG;
+
+  hsq::AppendArgs a{};
+  a.k = {k->data, k->token_stride, k->head_stride};
+  a.v = {v->data, v->token_stride, v->head_stride};
+  uintptr_t bits = view_bits(*k, tokens, kv_heads, es) | view_bits(*v, tokens, kv_heads, es);
+  if (q) {
+    a.q = {q->data, q->token_stride, q->head_stride};
+    a.q_out = {q_out->data, q_out->token_stride, q_out->head_stride};
+    bits |= view_bits(*q, tokens, q_heads, es) | view_bits(*q_out, tokens, q_heads, es);
+  }
+  // a cache piece is V elements of cs bytes, at most 16 bytes an access: its bits
+  // scaled to the input's size; an fp32 cache of bf16 inputs is written in whole
+  // 16-byte pieces or by elements
+  const uintptr_t cbits =
+      reinterpret_cast<uintptr_t>(cache->k) | reinterpret_cast<uintptr_t>(cache->v) |
+      (static_cast<uintptr_t>((cache->pages > 1 ? cache->page_stride : 0) | (cache->page_size > 1 ? cache->slot_stride : 0) |
+                              (kv_heads > 1 ? cache->head_stride : 0)) * cs);
+  bits |= cs <= es ? cbits * (es / cs) : (cbits % 16 ? 1 : 0);
+  a.kc = {cache->k, cache->page_stride, cache->slot_stride, cache->head_stride, cache->k_scale};
+  a.vc = {cache->v, cache->page_stride, cache->slot_stride, cache->head_stride, cache->v_scale};
+  a.rot = rope_table(rot, pos);
+  a.table = seqs->block_table; a.table_ld = seqs->table_ld;
+  a.lens = seqs->cache_lens; a.cu = seqs->cu_seqlens;
+  a.tokens = tokens; a.seqs = seqs->count;
+  a.q_heads = q_heads; a.kv_heads = kv_heads; a.dim = head_dim;
+  a.pages = cache->pages; a.page_size = cache->page_size; a.max_pages = seqs->max_pages;
+  a.q_in_place = in_place ? 1 : 0;
+  const int pairs = rot ? rot->pairs : 0;
+  const int w = piece_width(dtype, head_dim, pairs, bits);
+  a.units = pairs / w + (head_dim - 2 * pairs) / w;
+  split_heads(tokens, a.units, q_heads + 2 * kv_heads, a.splits, a.per_split);
+  if (static_cast<long long>(tokens) * a.splits * a.units > (1ll << 38)) return HSQ_ERR_UNSUPPORTED;
+  const bool adj = rot && rot->interleaved;
+  cudaError_t e;
+  if (dtype == HSQ_BF16)
+    e = w == 8 ? launch_append<__nv_bfloat16, 8>(a, cache->dtype, adj, stream)
+        : w == 4 ? launch_append<__nv_bfloat16, 4>(a, cache->dtype, adj, stream)
+                 : launch_append<__nv_bfloat16, 1>(a, cache->dtype, adj, stream);
+  else
+    e = w == 4 ? launch_append<float, 4>(a, cache->dtype, adj, stream)
+               : launch_append<float, 1>(a, cache->dtype, adj, stream);
+  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? HSQ_OK : HSQ_ERR_CUDA;
+}
 
 // ------------------------------------------------------------------ NVFP4 variant
 // Block-scaled GEMM tile: 128 tokens x HSQ_FP4_BN outputs (hsq_fp4.cuh).
@@ -1540,6 +1938,14 @@ hsq_status hsq_fp4_linear_forward(const uint8_t* x_codes, const uint8_t* x_sf, c
                                   const uint8_t* w_codes, const uint8_t* w_sf, const float* w_gs,
                                   const void* L2_bf16, const void* bias_bf16, int M, int N, int K, int r, void* Y,
                                   hsq_out_dtype out, cudaStream_t stream) {
+  return hsq_fp4_linear_forward_ep(x_codes, x_sf, x_gs, U, w_codes, w_sf, w_gs, L2_bf16, bias_bf16, M, N, K, r, Y, out,
+                                   nullptr, stream);
+}
+
+hsq_status hsq_fp4_linear_forward_ep(const uint8_t* x_codes, const uint8_t* x_sf, const float* x_gs, const float* U,
+                                     const uint8_t* w_codes, const uint8_t* w_sf, const float* w_gs,
+                                     const void* L2_bf16, const void* bias_bf16, int M, int N, int K, int r, void* Y,
+                                     hsq_out_dtype out, const hsq_epilogue* ep, cudaStream_t stream) {
   hsq_status st = fp4_check(M, K, r);
   if (st != HSQ_OK) return st;
   if (N < 1 || N > kMaxDim) return HSQ_ERR_INVALID_ARG;
@@ -1551,6 +1957,8 @@ hsq_status hsq_fp4_linear_forward(const uint8_t* x_codes, const uint8_t* x_sf, c
       !aligned16(w_gs) || !aligned16(Y) || (U && !aligned16(U)) || (L2_bf16 && !aligned16(L2_bf16)) ||
       (bias_bf16 && !aligned16(bias_bf16)))
     return HSQ_ERR_ALIGNMENT;
+  st = check_epilogue(&ep, M, N, Y, out);
+  if (st != HSQ_OK) return st;
   using Cfg = CfgFp4;
   const int Kq = fp4_kq(K);
   CUtensorMap tm_a, tm_b, tm_y;
@@ -1567,6 +1975,8 @@ hsq_status hsq_fp4_linear_forward(const uint8_t* x_codes, const uint8_t* x_sf, c
   a.tiles_n = (N + Cfg::BN - 1) / Cfg::BN;
   a.out_f32 = out == HSQ_OUT_F32 ? 1 : 0;
   a.limit_ns = wait_limit_ns();
+  a.Y = Y;
+  if (ep) a.epi = epi_args(*ep);
   static std::mutex mu;
   static bool attr_set[64] = {false};
   int dev = 0;
@@ -1575,6 +1985,8 @@ hsq_status hsq_fp4_linear_forward(const uint8_t* x_codes, const uint8_t* x_sf, c
     std::lock_guard<std::mutex> lk(mu);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
       if (cudaFuncSetAttribute(hsq::fp4_gemm_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Cfg::SMEM_BYTES) != cudaSuccess ||
+          cudaFuncSetAttribute(hsq::fp4_gemm_kernel<Cfg, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                Cfg::SMEM_BYTES) != cudaSuccess)
         return HSQ_ERR_CUDA;
       if (dev >= 0 && dev < 64) attr_set[dev] = true;
@@ -1582,8 +1994,8 @@ hsq_status hsq_fp4_linear_forward(const uint8_t* x_codes, const uint8_t* x_sf, c
   }
   const int tiles = a.tiles_m * a.tiles_n;
   const int grid = std::min(tiles, device_sm_count());
-  if (launch_pdl(false, hsq::fp4_gemm_kernel<Cfg>, dim3(grid), dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream, tm_a,
-                 tm_b, tm_y, a) != cudaSuccess)
+  if (launch_pdl(false, ep ? hsq::fp4_gemm_kernel<Cfg, true> : hsq::fp4_gemm_kernel<Cfg>, dim3(grid),
+                 dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream, tm_a, tm_b, tm_y, a) != cudaSuccess)
     return HSQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? HSQ_OK : HSQ_ERR_CUDA;
 }

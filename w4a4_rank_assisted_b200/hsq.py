@@ -25,10 +25,16 @@ HSQ_ERR_UNSUPPORTED = 3
 HSQ_ERR_CUDA = 4
 HSQ_ERR_TIMEOUT = 5
 HSQ_ERR_SCRATCH_LIMIT = 6
+HSQ_ERR_BAD_PAGE = 7
 #: Size of the built-in scratch array of hsq_linear_forward_noalloc.
 HSQ_NOALLOC_SCRATCH_BYTES = 16 << 20
 HSQ_OUT_BF16 = 0
 HSQ_OUT_F32 = 1
+HSQ_BF16, HSQ_F32, HSQ_E4M3 = 0, 1, 2
+HSQ_POS_I32, HSQ_POS_I64, HSQ_POS_F32 = 0, 1, 2
+HSQ_ROPE_MAX_AXES = 4
+#: Activations of the epilogue, by name (hsq_act).
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu_tanh": 2, "gelu_erf": 3, "silu": 4}
 
 #: Every symbol that include/hsq.h declares.
 EXPORTED = (
@@ -41,6 +47,8 @@ EXPORTED = (
     "hsq_lowrank_workspace_bytes", "hsq_lowrank_init",
     "hsq_fp4_codes_bytes", "hsq_fp4_scales_bytes", "hsq_fp4_pack_weights", "hsq_fp4_quantize_act",
     "hsq_fp4_linear_forward",
+    "hsq_linear_forward_ep", "hsq_linear_forward_x_ep", "hsq_linear_forward_fused_ep", "hsq_fp4_linear_forward_ep",
+    "hsq_rope", "hsq_kv_append",
 )
 
 
@@ -48,6 +56,37 @@ class HsqError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
         super().__init__(f"{what} failed: {status_string(status)}")
+
+
+class _CEpilogue(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int), ("mul", ctypes.c_void_p), ("mul_dtype", ctypes.c_int),
+                ("mul_rows", ctypes.c_int), ("mul_ld", ctypes.c_longlong), ("residual", ctypes.c_void_p),
+                ("residual_dtype", ctypes.c_int), ("residual_ld", ctypes.c_longlong)]
+
+
+class _CHeads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
+class _CRotation(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("pair_axis", ctypes.c_char_p), ("pairs", ctypes.c_int),
+                ("n_axes", ctypes.c_int), ("interleaved", ctypes.c_int), ("transpose", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class _CPositions(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("type", ctypes.c_int), ("rows", ctypes.c_int), ("ld", ctypes.c_longlong)]
+
+
+class _CPagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("page_stride", ctypes.c_longlong), ("slot_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class _CSequences(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("cache_lens", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p),
+                ("count", ctypes.c_int), ("max_pages", ctypes.c_int), ("table_ld", ctypes.c_longlong)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -113,6 +152,18 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.hsq_fp4_quantize_act.restype = i
     lib.hsq_fp4_linear_forward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, i, vp]
     lib.hsq_fp4_linear_forward.restype = i
+    lib.hsq_linear_forward_ep.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, i, vp, vp, sz, vp]
+    lib.hsq_linear_forward_ep.restype = i
+    lib.hsq_linear_forward_x_ep.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, i, vp, vp, sz, vp]
+    lib.hsq_linear_forward_x_ep.restype = i
+    lib.hsq_linear_forward_fused_ep.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, i, vp, vp]
+    lib.hsq_linear_forward_fused_ep.restype = i
+    lib.hsq_fp4_linear_forward_ep.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, i, vp, vp]
+    lib.hsq_fp4_linear_forward_ep.restype = i
+    lib.hsq_rope.argtypes = [vp, vp, i, i, i, i, vp, vp, vp]
+    lib.hsq_rope.restype = i
+    lib.hsq_kv_append.argtypes = [vp, vp, vp, vp, i, i, i, i, i, vp, vp, vp, vp, vp]
+    lib.hsq_kv_append.restype = i
     _lib = lib
     return lib
 
@@ -240,6 +291,241 @@ def hsq_linear_forward_fused(X, s, L1, w_codes, w_scales, L2, bias, M, N, K, r, 
                                            _ptr(L2), _ptr(bias), M, N, K, r, group, _ptr(Y), int(out),
                                            _stream(stream)),
            "hsq_linear_forward_fused")
+
+
+# ---------------------------------------------------------------- forwards with an epilogue
+def _out_dtype(t: torch.Tensor, what: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return HSQ_OUT_BF16
+    if t.dtype == torch.float32:
+        return HSQ_OUT_F32
+    raise ValueError(f"{what} is bfloat16 or float32, not {t.dtype}")
+
+
+class Epilogue:
+    """What a forward does to its result before it is rounded and written:
+    ``act(z) * mul + residual`` (hsq_epilogue).  ``act``: a name of ACTIVATIONS.
+    ``mul``: rows of N values, token m takes row ``m // mul_rows``; ``residual``:
+    M rows of N values (Y itself adds onto it in place).  Both may be column
+    ranges of wider tensors (last dimension dense, row stride a multiple of 8).
+    The object keeps the tensors and is reused from call to call."""
+
+    def __init__(self, act: str = "none", mul: Optional[torch.Tensor] = None, mul_rows: int = 1,
+                 residual: Optional[torch.Tensor] = None):
+        if act not in ACTIVATIONS:
+            raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTIVATIONS)})")
+        self.act, self.mul, self.mul_rows, self.residual = act, mul, int(mul_rows), residual
+        c = self._c = _CEpilogue(act=ACTIVATIONS[act], mul_rows=self.mul_rows)
+        for name, t in (("mul", mul), ("residual", residual)):
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError("libhsq takes CUDA tensors only")
+            if t.dim() != 2 or t.stride(1) != 1:
+                raise ValueError(f"{name} is a matrix with a dense last dimension")
+            setattr(c, name, t.data_ptr())
+            setattr(c, name + "_dtype", _out_dtype(t, name))
+            setattr(c, name + "_ld", t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8)
+
+    def _for(self, Y: torch.Tensor, M: int, N: int):
+        """The C struct, once the operands' shapes and device are those of Y."""
+        if self.mul is not None and (self.mul_rows < 1 or tuple(self.mul.shape) != (-(-M // self.mul_rows), N)):
+            raise ValueError(f"mul has {tuple(self.mul.shape)} values; {M} tokens at {self.mul_rows} a row, "
+                             f"{N} outputs")
+        if self.residual is not None and tuple(self.residual.shape) != (M, N):
+            raise ValueError(f"residual is {tuple(self.residual.shape)}, Y is {(M, N)}")
+        for t in (self.mul, self.residual):
+            if t is not None and t.device != Y.device:
+                raise ValueError("the epilogue's operands live on another device than Y")
+        return ctypes.byref(self._c)
+
+
+def _ep(epilogue: Optional[Epilogue], Y, M, N):
+    return None if epilogue is None else epilogue._for(Y, M, N)
+
+
+def hsq_linear_forward_ep(x_codes, x_scales, U, w_codes, w_scales, w_e4m3, L2, bias, M, N, K, r, Y,
+                          epilogue: Optional[Epilogue], out: int = HSQ_OUT_BF16, workspace=None, ws_bytes: int = 0,
+                          group=GROUP, stream=None) -> None:
+    """hsq_linear_forward (w_e4m3 None) or hsq_linear_forward_pre with an epilogue."""
+    _check(load().hsq_linear_forward_ep(_ptr(x_codes), _ptr(x_scales), _ptr(U), _ptr(w_codes), _ptr(w_scales),
+                                        _ptr(w_e4m3), _ptr(L2), _ptr(bias), M, N, K, r, group, _ptr(Y), int(out),
+                                        _ep(epilogue, Y, M, N), _ptr(workspace), int(ws_bytes), _stream(stream)),
+           "hsq_linear_forward_ep")
+
+
+def hsq_linear_forward_x_ep(X, s, L1, w_codes, w_scales, w_e4m3, L2, bias, M, N, K, r, Y,
+                            epilogue: Optional[Epilogue], out: int = HSQ_OUT_BF16, workspace=None, ws_bytes: int = 0,
+                            group=GROUP, stream=None) -> None:
+    """hsq_linear_forward_x with an epilogue."""
+    _check(load().hsq_linear_forward_x_ep(_ptr(X), _ptr(s), _ptr(L1), _ptr(w_codes), _ptr(w_scales), _ptr(w_e4m3),
+                                          _ptr(L2), _ptr(bias), M, N, K, r, group, _ptr(Y), int(out),
+                                          _ep(epilogue, Y, M, N), _ptr(workspace), int(ws_bytes), _stream(stream)),
+           "hsq_linear_forward_x_ep")
+
+
+def hsq_linear_forward_fused_ep(X, s, L1, w_codes, w_scales, L2, bias, M, N, K, r, Y, epilogue: Optional[Epilogue],
+                                out: int = HSQ_OUT_BF16, group=GROUP, stream=None) -> None:
+    """hsq_linear_forward_fused with an epilogue."""
+    _check(load().hsq_linear_forward_fused_ep(_ptr(X), _ptr(s), _ptr(L1), _ptr(w_codes), _ptr(w_scales), _ptr(L2),
+                                              _ptr(bias), M, N, K, r, group, _ptr(Y), int(out),
+                                              _ep(epilogue, Y, M, N), _stream(stream)),
+           "hsq_linear_forward_fused_ep")
+
+
+def hsq_fp4_linear_forward_ep(x_codes, x_sf, x_gs, U, w_codes, w_sf, w_gs, L2, bias, M, N, K, r, Y,
+                              epilogue: Optional[Epilogue], out: int = HSQ_OUT_BF16, stream=None) -> None:
+    """hsq_fp4_linear_forward with an epilogue."""
+    _check(load().hsq_fp4_linear_forward_ep(_ptr(x_codes), _ptr(x_sf), _ptr(x_gs), _ptr(U), _ptr(w_codes),
+                                            _ptr(w_sf), _ptr(w_gs), _ptr(L2), _ptr(bias), M, N, K, r, _ptr(Y),
+                                            int(out), _ep(epilogue, Y, M, N), _stream(stream)),
+           "hsq_fp4_linear_forward_ep")
+
+
+# ---------------------------------------------------------------- rotary positions, cache append
+_HEAD_DTYPES = {torch.bfloat16: HSQ_BF16, torch.float32: HSQ_F32}
+_CACHE_DTYPES = {**_HEAD_DTYPES, torch.float8_e4m3fn: HSQ_E4M3}
+_POS_DTYPES = {torch.int32: HSQ_POS_I32, torch.int64: HSQ_POS_I64, torch.float32: HSQ_POS_F32}
+
+
+class Rotation:
+    """A rotation of heads by positions (hsq_rotation): ``freqs`` [pairs] fp32,
+    ``pair_axes`` the axis of every pair (None: one axis).  The object keeps the
+    frequencies and is reused from call to call."""
+
+    def __init__(self, freqs: torch.Tensor, pair_axes=None, interleaved: bool = False, transpose: bool = False,
+                 scale: float = 1.0):
+        if not freqs.is_cuda or freqs.dtype != torch.float32 or freqs.dim() != 1 or not freqs.is_contiguous():
+            raise ValueError("freqs is a contiguous float32 CUDA vector")
+        axes = [0] * freqs.numel() if pair_axes is None else [int(a) for a in pair_axes]
+        if len(axes) != freqs.numel() or not axes:
+            raise ValueError(f"{freqs.numel()} frequencies and {len(axes)} pair axes")
+        if min(axes) < 0 or max(axes) >= HSQ_ROPE_MAX_AXES:
+            raise ValueError(f"axes are 0 .. {HSQ_ROPE_MAX_AXES - 1}")
+        self.freqs, self.pairs, self.n_axes = freqs, len(axes), max(axes) + 1
+        self.interleaved, self.transpose, self.scale = bool(interleaved), bool(transpose), float(scale)
+        self._axes = bytes(axes)
+        self._c = _CRotation(freqs=freqs.data_ptr(), pair_axis=self._axes, pairs=self.pairs, n_axes=self.n_axes,
+                             interleaved=int(self.interleaved), transpose=int(self.transpose), scale=self.scale)
+
+
+def _heads(t: torch.Tensor, name: str, shape=None) -> _CHeads:
+    if not t.is_cuda:
+        raise ValueError("libhsq takes CUDA tensors only")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} is [tokens, heads, head_dim] with a dense last dimension")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
+    return _CHeads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _positions(p: torch.Tensor, rotation: Rotation) -> _CPositions:
+    if not p.is_cuda:
+        raise ValueError("libhsq takes CUDA tensors only")
+    if p.dtype not in _POS_DTYPES:
+        raise ValueError(f"positions are int32, int64 or float32, not {p.dtype}")
+    if p.dim() == 1:
+        p = p[:, None]
+    if p.dim() != 2 or p.shape[1] != rotation.n_axes or (p.shape[1] > 1 and p.stride(1) != 1):
+        raise ValueError(f"positions are [rows, {rotation.n_axes}] with a dense last dimension")
+    return _CPositions(p.data_ptr(), _POS_DTYPES[p.dtype], p.shape[0],
+                       p.stride(0) if p.shape[0] > 1 else p.shape[1])
+
+
+def _one_device(*tensors) -> torch.device:
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError("the call's tensors live on different devices")
+    return dev
+
+
+def _on_device(dev: torch.device, stream, call):
+    """call(stream) with the tensors' device current; stream None: its current stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return call(_stream(stream))
+    return call(_stream(stream))
+
+
+def hsq_rope(x: torch.Tensor, y: torch.Tensor, positions: torch.Tensor, rotation: Rotation, stream=None) -> None:
+    """y = x rotated by its positions: x and y [tokens, heads, head_dim] (any token
+    and head strides; y may be x), positions [rows] or [rows, axes], token t taking
+    row t % rows.  With rotation.transpose the gradient of that map."""
+    h = _heads(x, "x")
+    if x.dtype not in _HEAD_DTYPES or y.dtype != x.dtype:
+        raise ValueError("x and y are both bfloat16 or both float32")
+    hy = _heads(y, "y", x.shape)
+    T, H, D = x.shape
+    pos = _positions(positions, rotation)
+    dev = _one_device(x, y, positions, rotation.freqs)
+    ref = ctypes.byref
+    _check(_on_device(dev, stream, lambda s: load().hsq_rope(
+        ref(h), ref(hy), _HEAD_DTYPES[x.dtype], T, H, D, ref(rotation._c), ref(pos), s)), "hsq_rope")
+
+
+def hsq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  block_table: torch.Tensor, cache_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                  rotation: Optional[Rotation] = None, positions: Optional[torch.Tensor] = None,
+                  q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """Appends the new tokens' k and v [tokens, kv_heads, head_dim] to the paged
+    caches [pages, page_size, kv_heads, head_dim] (any order of pages, slots and
+    heads in memory), k rotated, and writes q [tokens, q_heads, head_dim] rotated to
+    q_out.  block_table int32 [sequences, max_pages], cache_lens int32
+    [sequences], cu_seqlens int32 [sequences + 1] or None for one token per
+    sequence.  See include/hsq.h."""
+    if k.dtype not in _HEAD_DTYPES or v.dtype != k.dtype:
+        raise ValueError("k and v are both bfloat16 or both float32")
+    hk, hv = _heads(k, "k"), _heads(v, "v", k.shape)
+    T, H, D = k.shape
+    hq = hqo = None
+    q_heads = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        if q.dtype != k.dtype or q_out.dtype != k.dtype:
+            raise ValueError("q, q_out and k have one type")
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.shape[1] < 1:
+            raise ValueError(f"q is {tuple(q.shape)}, k is {tuple(k.shape)}")
+        hq, hqo = _heads(q, "q"), _heads(q_out, "q_out", q.shape)
+        q_heads = q.shape[1]
+    if k_cache.dtype not in _CACHE_DTYPES or v_cache.dtype != k_cache.dtype:
+        raise ValueError("the caches are both bfloat16, float32 or float8_e4m3fn")
+    if k_cache.dim() != 4 or k_cache.shape[2:] != k.shape[1:] or v_cache.shape != k_cache.shape:
+        raise ValueError(f"the caches are [pages, page_size, {H}, {D}], both")
+    if v_cache.stride() != k_cache.stride() or (D > 1 and k_cache.stride(3) != 1):
+        raise ValueError("the caches have equal strides and a dense last dimension")
+    ints = [("block_table", block_table, 2), ("cache_lens", cache_lens, 1)]
+    if cu_seqlens is not None:
+        ints.append(("cu_seqlens", cu_seqlens, 1))
+    for name, t, dims in ints:
+        if t.dtype != torch.int32 or t.dim() != dims or (t.numel() > 1 and t.shape[-1] > 1 and t.stride(-1) != 1):
+            raise ValueError(f"{name} is an int32 tensor of {dims} dimension(s), dense in the last")
+    B = cache_lens.shape[0]
+    if block_table.shape[0] != B or (cu_seqlens is not None and cu_seqlens.shape[0] != B + 1):
+        raise ValueError(f"{B} sequences, block_table {tuple(block_table.shape)}"
+                         + ("" if cu_seqlens is None else f", cu_seqlens {tuple(cu_seqlens.shape)}"))
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (H,) or not t.is_contiguous()):
+            raise ValueError(f"{name} is float32 [{H}]")
+    if positions is not None and rotation is None:
+        raise ValueError("positions without a rotation")
+    pos = None if positions is None else _positions(positions, rotation)
+    dev = _one_device(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens, positions, q, q_out, k_scale,
+                      v_scale, None if rotation is None else rotation.freqs)
+    opt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    cache = _CPagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _CACHE_DTYPES[k_cache.dtype], k_cache.shape[0],
+                         k_cache.shape[1], k_cache.stride(0), k_cache.stride(1), k_cache.stride(2), opt(k_scale),
+                         opt(v_scale))
+    seqs = _CSequences(block_table.data_ptr(), cache_lens.data_ptr(), opt(cu_seqlens), B, block_table.shape[1],
+                       block_table.stride(0) if B > 1 else block_table.shape[1])
+    ref = lambda c: None if c is None else ctypes.byref(c)  # noqa: E731
+    _check(_on_device(dev, stream, lambda s: load().hsq_kv_append(
+        ref(hk), ref(hv), ref(hq), ref(hqo), _HEAD_DTYPES[k.dtype], T, q_heads, H, D,
+        None if rotation is None else ctypes.byref(rotation._c), ref(pos), ref(cache), ref(seqs), s)),
+        "hsq_kv_append")
 
 
 def _sm_count() -> int:
@@ -411,9 +697,14 @@ class ActBuffers:
 
 
 def forward_fused(layer: PackedLinear, X: torch.Tensor, Y: torch.Tensor, out: int = HSQ_OUT_BF16,
-                  stream=None) -> torch.Tensor:
+                  stream=None, epilogue: Optional[Epilogue] = None) -> torch.Tensor:
     """One forward of the layer in a single launch (decode sizes, see
-    hsq_linear_forward_fused)."""
+    hsq_linear_forward_fused), with an epilogue where one is given."""
+    if epilogue is not None:
+        hsq_linear_forward_fused_ep(X, layer.s, layer.L1, layer.w_codes, layer.w_scales, layer.L2, layer.bias,
+                                    X.shape[0], layer.N, layer.K, layer.r, Y, epilogue, out=out, group=layer.group,
+                                    stream=stream)
+        return Y
     hsq_linear_forward_fused(X, layer.s, layer.L1, layer.w_codes, layer.w_scales, layer.L2, layer.bias,
                              X.shape[0], layer.N, layer.K, layer.r, Y, out=out, group=layer.group,
                              stream=stream)
@@ -421,10 +712,16 @@ def forward_fused(layer: PackedLinear, X: torch.Tensor, Y: torch.Tensor, out: in
 
 
 def forward_x(layer: PackedLinear, X: torch.Tensor, Y: torch.Tensor, workspace: torch.Tensor,
-              out: int = HSQ_OUT_BF16, stream=None) -> torch.Tensor:
-    """The activation step and the forward in one call (hsq_linear_forward_x);
-    `workspace` of at least layer.workspace_x(M) bytes."""
+              out: int = HSQ_OUT_BF16, stream=None, epilogue: Optional[Epilogue] = None) -> torch.Tensor:
+    """The activation step and the forward in one call (hsq_linear_forward_x), with
+    an epilogue where one is given; `workspace` of at least layer.workspace_x(M)
+    bytes."""
     M = X.shape[0]
+    if epilogue is not None:
+        hsq_linear_forward_x_ep(X, layer.s, layer.L1, layer.w_codes, layer.w_scales, layer.w_e4m3, layer.L2,
+                                layer.bias, M, layer.N, layer.K, layer.r, Y, epilogue, out=out, workspace=workspace,
+                                ws_bytes=workspace.numel(), group=layer.group, stream=stream)
+        return Y
     hsq_linear_forward_x(X, layer.s, layer.L1, layer.w_codes, layer.w_scales, layer.w_e4m3, layer.L2, layer.bias,
                          M, layer.N, layer.K, layer.r, Y, out=out, workspace=workspace, ws_bytes=workspace.numel(),
                          group=layer.group, stream=stream)
@@ -432,15 +729,21 @@ def forward_x(layer: PackedLinear, X: torch.Tensor, Y: torch.Tensor, workspace: 
 
 
 def forward(layer: PackedLinear, X: torch.Tensor, act: ActBuffers, Y: torch.Tensor,
-            workspace: Optional[torch.Tensor] = None, out: int = HSQ_OUT_BF16, stream=None) -> torch.Tensor:
-    """One forward of the layer: the activation step, then the GEMM + epilogue."""
+            workspace: Optional[torch.Tensor] = None, out: int = HSQ_OUT_BF16, stream=None,
+            epilogue: Optional[Epilogue] = None) -> torch.Tensor:
+    """One forward of the layer: the activation step, then the GEMM + epilogue
+    (U L2 + bias, and where one is given act, mul and residual)."""
     M = X.shape[0]
     if act.group != layer.group:
         raise ValueError("activation buffers and packed layer use different group sizes")
     hsq_quantize_act(X, layer.s, layer.L1, M, layer.K, layer.r, act.x_codes, act.x_scales, act.U,
                      group=layer.group, stream=stream)
     ws_bytes = 0 if workspace is None else workspace.numel()
-    if layer.w_e4m3 is not None:
+    if epilogue is not None:
+        hsq_linear_forward_ep(act.x_codes, act.x_scales, act.U, layer.w_codes, layer.w_scales, layer.w_e4m3,
+                              layer.L2, layer.bias, M, layer.N, layer.K, layer.r, Y, epilogue, out=out,
+                              workspace=workspace, ws_bytes=ws_bytes, group=layer.group, stream=stream)
+    elif layer.w_e4m3 is not None:
         hsq_linear_forward_pre(act.x_codes, act.x_scales, act.U, layer.w_codes, layer.w_scales, layer.w_e4m3,
                                layer.L2, layer.bias, M, layer.N, layer.K, layer.r, Y, out=out, workspace=workspace,
                                ws_bytes=ws_bytes, group=layer.group, stream=stream)
@@ -517,11 +820,17 @@ class Fp4ActBuffers:
 
 
 def fp4_forward(layer: Fp4Linear, X: torch.Tensor, act: Fp4ActBuffers, Y: torch.Tensor,
-                out: int = HSQ_OUT_BF16, stream=None) -> torch.Tensor:
-    """One NVFP4 forward: the activation step, then the block-scaled GEMM + epilogue."""
+                out: int = HSQ_OUT_BF16, stream=None, epilogue: Optional[Epilogue] = None) -> torch.Tensor:
+    """One NVFP4 forward: the activation step, then the block-scaled GEMM + epilogue
+    (U L2 + bias, and where one is given act, mul and residual)."""
     M = X.shape[0]
     hsq_fp4_quantize_act(X, layer.s, layer.L1, M, layer.K, layer.r, act.x_codes, act.x_sf, act.x_gs, act.U,
                          stream=stream)
+    if epilogue is not None:
+        hsq_fp4_linear_forward_ep(act.x_codes, act.x_sf, act.x_gs, act.U, layer.w_codes, layer.w_sf, layer.w_gs,
+                                  layer.L2, layer.bias, M, layer.N, layer.K, layer.r, Y, epilogue, out=out,
+                                  stream=stream)
+        return Y
     hsq_fp4_linear_forward(act.x_codes, act.x_sf, act.x_gs, act.U, layer.w_codes, layer.w_sf, layer.w_gs,
                            layer.L2, layer.bias, M, layer.N, layer.K, layer.r, Y, out=out, stream=stream)
     return Y
