@@ -41,7 +41,6 @@ struct Fp4Args {
   int out_f32;
   uint64_t limit_ns;
   EpiArgs epi;  // kernels with EPI: act, mul and residual (hsq_epilogue.cuh)
-  void* Y;      // ... which write Y without the tensor map
 };
 
 // Tile 128 tokens x BN outputs; a stage is K = 256 (KCS = 4 chunks of K = 64).
@@ -244,6 +243,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++nt) {
       const int tm = t % args.tiles_m, tn = t / args.tiles_m;
       const int tb = nt % NTM;
+      if constexpr (EPI) epi_prefetch<128>(args.epi, tm * BM + q * 32, tn * BN + part * 128, args.M, args.N);
       if (!wait_warp(&tfull[tb], (nt / NTM) & 1, wp)) break;
       const int lb = nt % Cfg::LR_BUFS;
       if (!wait_warp(&lrfull[lb], (nt / Cfg::LR_BUFS) & 1, wp)) break;
@@ -296,22 +296,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
         auto y = [&](int c) { return __uint_as_float(v[c >> 4][c & 15]); };
         if constexpr (EPI) {
-          // 32 rows x 32 fp32 columns at a time through the staging buffer into row
-          // order, where mul and residual are read and Y is written
+          if (lane == 0) bulk_wait_read_all();  // the last tile's stores have left the buffer
+          __syncwarp();
+          epi_apply_rows<4>(args.epi, stg, y0, n0, args.M, args.N, [&](int lo, int hi, auto&& g) {
 #pragma unroll
-          for (int pz = 0; pz < 4; ++pz) {
-            EpiBox box;
-            epi_load_box(args.epi, y0, n0 + 32 * pz, args.M, args.N, box);
-            __syncwarp();  // the previous box has been read
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<float4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-                  make_float4(y(32 * pz + 4 * c), y(32 * pz + 4 * c + 1), y(32 * pz + 4 * c + 2),
-                              y(32 * pz + 4 * c + 3));
-            __syncwarp();
-            epi_store_box(args.epi, stg, box, y0, n0 + 32 * pz, args.M, args.N, args.Y, args.out_f32);
-          }
-        } else
+            for (int j = 0; j < 128; j += 2)
+              if (j >= lo && j < hi) g(reinterpret_cast<float2*>(v[j >> 4])[(j & 15) >> 1], lane, j);
+          });
+        }
         // store: 32 rows x 128 bytes per TMA box, 128-byte swizzled staging
         if (!args.out_f32) {
 #pragma unroll

@@ -281,6 +281,12 @@ struct GemmCfg {
 template <class Base>
 struct GemmCfgEpi : Base {
   static constexpr bool EPI = true;
+  // Pairs of an operand requested at a time (tokens x outputs tiles).  64 spill a
+  // little next to 128 accumulators.  Measured, 32 and 64: mul 688 and 671 us on groups
+  // of 128 (M = 8192, K = 4096, N = 12288, 603 us without), where 64 spills 16 bytes;
+  // tanh gelu 92 and 96 us on groups of 64 (M = 4096, K = 1152, N = 4608, 83 us without),
+  // where it spills 200.
+  static constexpr int EPI_AHEAD = Base::PRE && Base::BPG == 2 ? 64 : 32;
 };
 
 // Unpack 16 packed bytes (32 codes) into two 16-byte int8 core-matrix rows
@@ -1141,6 +1147,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const int rbase = tr * TILE_M + static_cast<int>(crank) * BM + q * 32 + qd;  // row of i = 0 (row i adds 8i)
       const int col0 = tc * BN + h * CW + 2 * qc;  // column of block 0, first of the pair
       const bool lr_unit = Cfg::LR_MMA && args.lr_mma && g0 == 0;
+      if constexpr (Cfg::EPI && Cfg::TMA_STORE)
+        epi_prefetch<CW>(args.epi, tr * TILE_M + static_cast<int>(crank) * BM + q * 32, tc * BN + h * CW, args.M, args.N);
       float2 acc2[4 * NBLK];
 #pragma unroll
       for (int j = 0; j < 4 * NBLK; ++j) acc2[j] = make_float2(0.f, 0.f);
@@ -1352,33 +1360,25 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       }
       // the accumulators already hold U L2 + b (added by the tile's first unit)
       if constexpr (Cfg::TMA_STORE && Cfg::EPI) {
-        // The warp's 32 rows x 32 fp32 columns at a time go through its staging
-        // buffer (the fp32 layout below) into row order, where mul and residual
-        // are read and Y is written in whole 16-byte pieces; mul and residual are
-        // requested before the staging.
-        uint8_t* stg = ystage + dw * 4096;
-        const int y0 = tr * TILE_M + static_cast<int>(crank) * BM + q * 32;
-        const int x0 = tc * BN + h * CW;
+        // on the accumulators in place; rows and columns outside Y read the last row
+        // and the slice's first columns (the TMA unit clips them)
+        const int live = args.N - (tc * BN + h * CW);
+        size_t mrow[4], rrow[4];
 #pragma unroll
-        for (int pz = 0; pz < CW / 32; ++pz) {
-          EpiBox box;
-          epi_load_box(args.epi, y0, x0 + 32 * pz, args.M, args.N, box);
-          __syncwarp();  // the previous box has been read
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rl = qd + 8 * i;
-#pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-              const int c16 = 2 * kb + (qc >> 1);
-              *reinterpret_cast<float2*>(stg + rl * 128 + ((c16 ^ (rl & 7)) << 4) + (qc & 1) * 8) =
-                  acc2[i * NBLK + 4 * pz + kb];
-            }
-          }
-          __syncwarp();
-          epi_store_box(args.epi, stg, box, y0, x0 + 32 * pz, args.M, args.N, args.Y, args.out_f32);
+        for (int i = 0; i < 4; ++i) {
+          const int m = min(rbase + 8 * i, args.M - 1);
+          int mr = m;
+          if (args.epi.mul_rows != 1) mr = m / args.epi.mul_rows;
+          mrow[i] = static_cast<size_t>(mr) * args.epi.mul_ld + col0;
+          rrow[i] = static_cast<size_t>(m) * args.epi.res_ld + col0;
         }
-        __syncwarp();
-      } else if constexpr (Cfg::TMA_STORE) {
+        if (live > 0)
+          epi_apply_quads<4, NBLK, Cfg::EPI_AHEAD>(
+              args.epi, [&](int i, int b) -> float2& { return acc2[i * NBLK + b]; },
+              [&](int i, int b) { return mrow[i] + (8 * b < live ? 8 * b : 0); },
+              [&](int i, int b) { return rrow[i] + (8 * b < live ? 8 * b : 0); });
+      }
+      if constexpr (Cfg::TMA_STORE) {
         // Stage 32 rows x 128 bytes at a time in this warp's buffer, in the
         // 128-byte swizzled layout (16-byte chunk c of row r at chunk c ^ (r % 8),
         // so the quad-layout writes hit distinct banks), then one TMA store of
@@ -1449,27 +1449,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
       } else {
         // rows are output features n, columns are tokens m
+        if constexpr (Cfg::EPI)
+          epi_apply_columns<4, NBLK>(args.epi, [&](int i, int b) -> float2& { return acc2[i * NBLK + b]; },
+                                     [&](int i) { return min(rbase + 8 * i, args.N - 1); },
+                                     [&](int b) { return min(col0 + 8 * (b >> 1) + (b & 1), args.M - 1); });
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int n = rbase + 8 * i;
           if (n >= args.rows_r) continue;
-          float em[Cfg::EPI ? 2 * NBLK : 1], er[Cfg::EPI ? 2 * NBLK : 1];  // mul and residual, requested together
-          if constexpr (Cfg::EPI) {
-#pragma unroll
-            for (int t = 0; t < 2 * NBLK; ++t) {
-              const int m = col0 + 8 * (t >> 1) + (t & 1);
-              em[t] = m < args.M ? epi_mul_at(args.epi, m, n) : 0.f;
-              er[t] = m < args.M ? epi_res_at(args.epi, m, n) : 0.f;
-            }
-          }
 #pragma unroll
           for (int b = 0; b < NBLK; ++b) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int m = col0 + 8 * b + e;
               if (m < args.M) {
-                float v = e ? acc2[i * NBLK + b].y : acc2[i * NBLK + b].x;
-                if constexpr (Cfg::EPI) v = epi_value(args.epi, v, em[2 * b + e], er[2 * b + e]);
+                const float v = e ? acc2[i * NBLK + b].y : acc2[i * NBLK + b].x;
                 const size_t off = static_cast<size_t>(m) * args.N + n;
                 if (args.out_f32) static_cast<float*>(args.Y)[off] = v;
                 else static_cast<__nv_bfloat16*>(args.Y)[off] = __float2bfloat16_rn(v);

@@ -198,6 +198,18 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
     const int cw = warp - 1;
     const int ct = threadIdx.x - 32;
     grid_dep_wait();  // the activation codes (or X) come from the preceding kernel
+    // mul and residual of all the warp's rows at once, ahead of their sums: lane l
+    // holds those of its row cw + 15 l (at most 256 / 15 < 32 rows)
+    float emul[EPI ? MT : 1], eres[EPI ? MT : 1];
+    if constexpr (EPI) {
+      const int i = cw + kGemvComputeWarps * lane;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const bool in = i < nrows && m < a.M;
+        emul[m] = in ? epi_mul_at(a.epi, m, n0 + i) : 0.f;
+        eres[m] = in ? epi_res_at(a.epi, m, n0 + i) : 0.f;
+      }
+    }
     const float* Uv = a.U;  // U [M][r]: the activation step's, or this block's own (fused)
     if constexpr (RF < 0) {
       for (int i = ct; i < MT * W4; i += kGemvComputeWarps * 32) {
@@ -324,13 +336,6 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
            i += kGemvComputeWarps) {
       const uint4* wrow = reinterpret_cast<const uint4*>(ring + (static_cast<size_t>(s) * a.rs + (i - it * a.rs)) * rowbytes);
       const int n = n0 + i;
-      float em = 1.f, er = 0.f;  // lane m: the row's mul and residual for token m, requested ahead of its sums
-      if constexpr (EPI) {
-        if (lane < a.M && lane < MT) {
-          em = epi_mul_at(a.epi, lane, n);
-          er = epi_res_at(a.epi, lane, n);
-        }
-      }
       float acc[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[m] = 0.f;
@@ -387,11 +392,22 @@ __global__ void __launch_bounds__(kGemvThreads, 1)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
       const float bn = a.bias ? __bfloat162float(a.bias[n]) : 0.f;
+      if constexpr (EPI) {
+        // the row's operands from the lane that holds them; every lane has the sums
+        float em[MT], er[MT];
+        const int src = i / kGemvComputeWarps;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          em[m] = __shfl_sync(0xffffffffu, emul[m], src);
+          er[m] = __shfl_sync(0xffffffffu, eres[m], src);
+          acc[m] += bn;
+        }
+        epi_values(a.epi, acc, em, er);
+      }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (lane == m && m < a.M) {
-          float y = acc[m] + bn;
-          if constexpr (EPI) y = epi_value(a.epi, y, em, er);
+          const float y = EPI ? acc[m] : acc[m] + bn;
           const size_t off = static_cast<size_t>(m) * a.N + n;
           if (a.out_f32) static_cast<float*>(a.Y)[off] = y;
           else static_cast<__nv_bfloat16*>(a.Y)[off] = __float2bfloat16_rn(y);

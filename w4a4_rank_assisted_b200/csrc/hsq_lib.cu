@@ -1975,7 +1975,6 @@ hsq_status hsq_fp4_linear_forward_ep(const uint8_t* x_codes, const uint8_t* x_sf
   a.tiles_n = (N + Cfg::BN - 1) / Cfg::BN;
   a.out_f32 = out == HSQ_OUT_F32 ? 1 : 0;
   a.limit_ns = wait_limit_ns();
-  a.Y = Y;
   if (ep) a.epi = epi_args(*ep);
   static std::mutex mu;
   static bool attr_set[64] = {false};
