@@ -149,165 +149,180 @@ __device__ __forceinline__ void epi_prefetch(const EpiArgs& e, int m0, int n0, i
   if (e.res) rows(e.res, e.res_f32, e.res_ld, m);
 }
 
-// One operand's box under the warp's part of Y: 32 rows of 128 bytes (64 bf16 or 32
-// fp32 columns), eight lanes to a row, so that each access covers whole lines.
-// fetch requests HOLD of its 8 accesses into registers, land lays the box in the warp's
-// staging buffer (16-byte chunk c of row r at chunk c ^ (r % 8): the writes, and the
-// readers' pairs, touch 32 different banks).  Rows behind M read row M - 1 and columns
-// behind N the row's first ones: nothing outside the operand is read, and those
-// outputs are clipped by the TMA unit.
+// One operand's box under the warp's part of Y: 32 rows of 64 bytes (32 bf16 or 16
+// fp32 columns), copied asynchronously into 2 KB of the warp's staging buffer: 16-byte
+// chunk c of row r at chunk c ^ (r / 2 % 4) of its 64 bytes, so that eight rows' chunk
+// c fall into 32 different banks.  Rows behind M read row M - 1 and columns behind N
+// the row's first ones: nothing outside the operand is read, and those outputs are
+// clipped by the TMA unit.
 struct EpiOperand {
   const void* p;
   long long ld;
   int rows;  // tokens to a row
   bool f32;
 };
-template <int HOLD>
-struct EpiBox {
-  uint4 w[HOLD];
-  __device__ __forceinline__ void fetch(const EpiOperand& o, int y0, int n0, int M, int N, int part = 0) {
+__device__ __forceinline__ void epi_fetch(const EpiOperand& o, uint8_t* box, int y0, int n0, int M, int N) {
+  const int lane = lane_id(), c = lane & 3;
+  int n = n0 + c * (o.f32 ? 4 : 8);
+  if (n >= N) n = 0;
+  const char* base = static_cast<const char*>(o.p) + static_cast<size_t>(n) * (o.f32 ? 4 : 2);
+  const size_t pitch = static_cast<size_t>(o.ld) * (o.f32 ? 4 : 2);
+  auto rows = [&](auto&& row) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                       smem_u32(box + r * 64 + ((c ^ ((r >> 1) & 3)) << 4))),
+                   "l"(base + static_cast<size_t>(row(min(y0 + r, M - 1))) * pitch)
+                   : "memory");
+    }
+  };
+  if (o.rows == 1) rows([](int m) { return m; });
+  else rows([&](int m) { return m / o.rows; });
+}
+// Four 8 x 8 blocks of 16-bit elements, a row's address from each lane: lane l gets
+// elements 2 (l % 4), + 1 of row l / 4 of each.
+__device__ __forceinline__ void ldmatrix_x4(uint32_t saddr, uint32_t (&w)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(saddr)
+               : "memory");
+}
+__device__ __forceinline__ float2 epi_pair16(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// How the threads hold the warp's accumulators of 32 rows and 128 columns, and read a
+// box for them: use16 / use32 apply f(z, operand) to the pairs of neighbouring
+// columns in a box of 32 bf16 / 16 fp32 columns, the k-th of the 128.
+//   Quads: tcgen05.ld 16x256b: lane l has rows l / 4 + 8i and columns 8b + 2 (l % 4), + 1
+template <int NBLK>
+struct EpiQuads {
+  float2 (&acc)[4 * NBLK];
+  template <class F>
+  __device__ __forceinline__ void all(F&& f) {
+#pragma unroll
+    for (int j = 0; j < 4 * NBLK; ++j) f(acc[j]);
+  }
+  template <class F>
+  __device__ __forceinline__ void use16(const uint8_t* box, int k, F&& f) {
     const int lane = lane_id();
-    int n = n0 + (lane & 7) * (o.f32 ? 4 : 8);
-    if (n >= N) n = 0;
-    const char* base = static_cast<const char*>(o.p) + static_cast<size_t>(n) * (o.f32 ? 4 : 2);
-    const size_t pitch = static_cast<size_t>(o.ld) * (o.f32 ? 4 : 2);
-    const int m0 = y0 + 4 * HOLD * part + (lane >> 3);
-    if (o.rows == 1) {
 #pragma unroll
-      for (int i = 0; i < HOLD; ++i)
-        w[i] = *reinterpret_cast<const uint4*>(base + static_cast<size_t>(min(m0 + 4 * i, M - 1)) * pitch);
-    } else {
+    for (int i = 0; i < 4; ++i) {
+      // block b of row group i: its rows' addresses from lanes 8b .. 8b + 7
+      const int r = 8 * i + (lane & 7);
+      uint32_t w[4];
+      ldmatrix_x4(smem_u32(box + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4)), w);
 #pragma unroll
-      for (int i = 0; i < HOLD; ++i)
-        w[i] = *reinterpret_cast<const uint4*>(base + static_cast<size_t>(min(m0 + 4 * i, M - 1) / o.rows) * pitch);
+      for (int b = 0; b < 4; ++b) f(acc[i * NBLK + 4 * k + b], epi_pair16(w[b]));
     }
   }
-  // Defines the registers where nothing is fetched.  A conditional load alone leaves
-  // them live from the loop over tiles on, and the accumulators spill.
-  __device__ __forceinline__ void none() {
+  template <class F>
+  __device__ __forceinline__ void use32(const uint8_t* box, int k, F&& f) {
+    const int lane = lane_id(), qc = lane & 3;
 #pragma unroll
-    for (int i = 0; i < HOLD; ++i)
-      asm volatile("" : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w));
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        f(acc[i * NBLK + 2 * k + b],
+          *reinterpret_cast<const float2*>(box + r * 64 + (((2 * b + (qc >> 1)) ^ ((r >> 1) & 3)) << 4) + (qc & 1) * 8));
+    }
   }
-  __device__ __forceinline__ void put(uint8_t* stg, int part) const {
+};
+//   Rows: tcgen05.ld 32x32b: lane l has row l, v[c] its columns 16 c ..
+struct EpiRows {
+  uint32_t (&v)[8][16];
+  __device__ __forceinline__ float2& pair(int j) { return reinterpret_cast<float2*>(v[j >> 3])[j & 7]; }
+  template <class F>
+  __device__ __forceinline__ void all(F&& f) {
+#pragma unroll
+    for (int j = 0; j < 64; ++j) f(pair(j));
+  }
+  template <class F>
+  __device__ __forceinline__ void use16(const uint8_t* box, int k, F&& f) {
     const int lane = lane_id();
 #pragma unroll
-    for (int i = 0; i < HOLD; ++i) {
-      const int r = 4 * (HOLD * part + i) + (lane >> 3);
-      *reinterpret_cast<uint4*>(stg + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = w[i];
+    for (int c = 0; c < 4; ++c) {
+      const uint4 q = *reinterpret_cast<const uint4*>(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f(pair(16 * k + 4 * c + e), epi_pair16(w[e]));
     }
   }
-  // the box whose first part has been fetched, into stg
-  __device__ __forceinline__ void land(const EpiOperand& o, uint8_t* stg, int y0, int n0, int M, int N) {
-    __syncwarp();  // the box before has been read
-    put(stg, 0);
+  template <class F>
+  __device__ __forceinline__ void use32(const uint8_t* box, int k, F&& f) {
+    const int lane = lane_id();
 #pragma unroll
-    for (int part = 1; part < 8 / HOLD; ++part) {
-      fetch(o, y0, n0, M, N, part);
-      put(stg, part);
+    for (int c = 0; c < 4; ++c) {
+      const float4 q = *reinterpret_cast<const float4*>(box + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+      f(pair(8 * k + 2 * c), make_float2(q.x, q.y));
+      f(pair(8 * k + 2 * c + 1), make_float2(q.z, q.w));
     }
-    __syncwarp();
   }
 };
 
 // act(z) * mul + residual in place on the warp's accumulators of 32 rows y0 .. and 128
-// columns n0 ..: each(lo, hi, f) calls f(z, row, column) on the pairs of neighbouring
-// columns that the thread holds in lo .. hi - 1, as straight code on registers.  (A
-// rolled loop that reads the accumulators back from Tensor Memory or shared memory
-// took longer for every activation and operand: a warp shares its scheduler with one
-// other, so passes are bound by latency.)  A box is requested before the arithmetic on
-// the one before it, the first before the activation.
-template <int HOLD, class Each>
-__device__ __forceinline__ void epi_apply_rows(const EpiArgs& e, uint8_t* stg, int y0, int n0, int M, int N, Each&& each) {
+// columns n0 .. (n0 < N).  stg: the warp's 4 KB staging buffer, through which the
+// operands come in two boxes of 2 KB in turn, each requested while the one before it is
+// used, the first two ahead of the activation.
+//
+// The accumulators stay where they are, in straight code.  A warp shares its
+// scheduler with one other here, so a pass over them is bound by latency: rolled loops
+// that read them back from Tensor Memory or shared memory took longer for every
+// activation and operand.  No operand waits in registers: those loaded under a
+// condition stay live from the loop over tiles on, and the accumulators spill.
+// Bound by the activation's special-function instructions (two an element: 2 us per
+// 128 x 256 tile) and by instruction latency.  Measured with the activation step, us
+// (none / silu / mul / silu * mul / silu * mul + residual): 602 / 650 / 671 / 697 / 753 at
+// M = 8192, K = 4096, N = 12288, groups of 128; 83 / 96 / 97 / 107 / 117 at M = 4096, K =
+// 1152, N = 4608, groups of 64; NVFP4 at M = 4096, K = 4608, N = 1152: 95.8 / 98.7 / 99.6 /
+// 100.7 / 104.9.  (A pass of its own over Y and mul reads and writes 600 MB at the
+// first size: 92 us.)
+template <class Acc>
+__device__ __forceinline__ void epi_apply(const EpiArgs& e, uint8_t* stg, int y0, int n0, int M, int N, Acc&& acc) {
   const EpiOperand mul{e.mul, e.mul_ld, e.mul_rows, e.mul_f32 != 0}, res{e.res, e.res_ld, 1, e.res_f32 != 0};
-  EpiBox<HOLD> box;
-  if (mul.p) box.fetch(mul, y0, n0, M, N);
-  else if (res.p) box.fetch(res, y0, n0, M, N);
-  else box.none();
-  epi_act_each(e.act, [&](auto&& f) { each(0, 128, [&](float2& z, int, int) { f(z); }); });
+  // box k of an operand into buffer k % 2 (an operand has four or eight); one group
+  // each, empty where there is no operand
+  auto request = [&](const EpiOperand& o, int k) {
+    if (o.p) epi_fetch(o, stg + (k & 1) * 2048, y0, n0 + (o.f32 ? 16 : 32) * k, M, N);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (mul.p || res.p) {
+    if (lane_id() == 0) bulk_wait_read_all();  // the last tile's stores have left the buffer
+    __syncwarp();
+    if (mul.p) {
+      request(mul, 0);
+      request(mul, 1);
+    } else {
+      request(res, 0);
+      request(res, 1);
+    }
+  }
+  epi_act_each(e.act, [&](auto&& f) { acc.all(f); });
   auto boxes = [&](const EpiOperand& o, const EpiOperand& after, auto&& f) {
+    auto step = [&](int k, int n, auto&& use) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();  // the box is whole
+      use(stg + (k & 1) * 2048);
+      __syncwarp();  // ... and has been read
+      if (k + 2 < n) request(o, k + 2);
+      else request(after, k + 2 - n);
+    };
     if (!o.f32) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        box.land(o, stg, y0, n0 + 64 * k, M, N);
-        if (k == 0) box.fetch(o, y0, n0 + 64, M, N);
-        else if (after.p) box.fetch(after, y0, n0, M, N);
-        else box.none();
-        each(64 * k, 64 * k + 64, [&](float2& z, int r, int c) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(stg + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) +
-                                                               (c & 7) * 2);
-          f(z, make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)));
-        });
-      }
+      for (int k = 0; k < 4; ++k) step(k, 4, [&](const uint8_t* box) { acc.use16(box, k, f); });
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        box.land(o, stg, y0, n0 + 32 * k, M, N);
-        if (k < 3) box.fetch(o, y0, n0 + 32 * (k + 1), M, N);
-        else if (after.p) box.fetch(after, y0, n0, M, N);
-        else box.none();
-        each(32 * k, 32 * k + 32, [&](float2& z, int r, int c) {
-          f(z, *reinterpret_cast<const float2*>(stg + r * 128 + ((((c >> 2) & 7) ^ (r & 7)) << 4) + (c & 3) * 4));
-        });
-      }
+      for (int k = 0; k < 8; ++k) step(k, 8, [&](const uint8_t* box) { acc.use32(box, k, f); });
     }
   };
   const EpiOperand nothing{nullptr, 0, 1, false};
-  if (mul.p) boxes(mul, res, [](float2& a, const float2& m) { a = __fmul2_rn(a, m); });
-  if (res.p) boxes(res, nothing, [](float2& a, const float2& r) { a = __fadd2_rn(a, r); });
-  __syncwarp();  // the buffer has been read
+  if (mul.p) boxes(mul, res, [](float2& z, const float2& m) { z = __fmul2_rn(z, m); });
+  if (res.p) boxes(res, nothing, [](float2& z, const float2& r) { z = __fadd2_rn(z, r); });
 }
 
-// f(z, operand) on R x B pairs of accumulators z(i, b), whose operands lie at(i, b)
-// elements into p: `ahead` pairs are requested at a time, then used.
-template <int R, int B, int AHEAD, class Z, class At, class F>
-__device__ __forceinline__ void epi_quads_operand(const void* p, bool f32, Z&& z, At&& at, F&& f) {
-  static_assert((R * B) % AHEAD == 0, "whole batches");
-  if (!f32) {
-#pragma unroll
-    for (int j0 = 0; j0 < R * B; j0 += AHEAD) {
-      uint32_t w[AHEAD];
-#pragma unroll
-      for (int j = 0; j < AHEAD; ++j)
-        w[j] = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p) + at((j0 + j) % R, (j0 + j) / R));
-#pragma unroll
-      for (int j = 0; j < AHEAD; ++j)
-        f(z((j0 + j) % R, (j0 + j) / R),
-          make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)));
-    }
-  } else {
-#pragma unroll
-    for (int j0 = 0; j0 < R * B; j0 += AHEAD / 2) {
-      float2 w[AHEAD / 2];
-#pragma unroll
-      for (int j = 0; j < AHEAD / 2; ++j)
-        w[j] = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + at((j0 + j) % R, (j0 + j) / R));
-#pragma unroll
-      for (int j = 0; j < AHEAD / 2; ++j) f(z((j0 + j) % R, (j0 + j) / R), w[j]);
-    }
-  }
-}
-
-// act(z) * mul + residual in place on the thread's R x B pairs of accumulators z(i, b):
-// R rows, B pairs of neighbouring columns in each.  Straight code on registers: a
-// rolled loop that reads the accumulators back from Tensor Memory or shared memory
-// took longer for every activation and operand (a warp shares its scheduler with one
-// other, so its passes are bound by latency).  No conditional load: one that may
-// leave its register undefined keeps it live from the loop over tiles on, and the
-// accumulators spill.
-template <int R, int B, int AHEAD, class Z, class MulAt, class ResAt>
-__device__ __forceinline__ void epi_apply_quads(const EpiArgs& e, Z&& z, MulAt&& mul_at, ResAt&& res_at) {
-  epi_act_each(e.act, [&](auto&& f) {
-#pragma unroll
-    for (int j = 0; j < R * B; ++j) f(z(j % R, j / R));
-  });
-  if (e.mul)
-    epi_quads_operand<R, B, AHEAD>(e.mul, e.mul_f32 != 0, z, mul_at, [](float2& a, const float2& m) { a = __fmul2_rn(a, m); });
-  if (e.res)
-    epi_quads_operand<R, B, AHEAD>(e.res, e.res_f32 != 0, z, res_at, [](float2& a, const float2& r) { a = __fadd2_rn(a, r); });
-}
-
-// The same on accumulators of R output features feature(i) by 2 B tokens token(t),
+// act(z) * mul + residual in place on accumulators of R output features feature(i) by 2 B tokens token(t),
 // the pair z(i, b) holding tokens 2b and 2b + 1 of the thread: operands by elements, a
 // batch requested at a time.
 template <int R, int B, class T, class Z, class Feature, class Token, class F>

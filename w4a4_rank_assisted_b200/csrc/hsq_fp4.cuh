@@ -295,15 +295,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
         }
         auto y = [&](int c) { return __uint_as_float(v[c >> 4][c & 15]); };
-        if constexpr (EPI) {
-          if (lane == 0) bulk_wait_read_all();  // the last tile's stores have left the buffer
-          __syncwarp();
-          epi_apply_rows<4>(args.epi, stg, y0, n0, args.M, args.N, [&](int lo, int hi, auto&& g) {
-#pragma unroll
-            for (int j = 0; j < 128; j += 2)
-              if (j >= lo && j < hi) g(reinterpret_cast<float2*>(v[j >> 4])[(j & 15) >> 1], lane, j);
-          });
-        }
+        if constexpr (EPI) epi_apply(args.epi, stg, y0, n0, args.M, args.N, EpiRows{v});
         // store: 32 rows x 128 bytes per TMA box, 128-byte swizzled staging
         if (!args.out_f32) {
 #pragma unroll

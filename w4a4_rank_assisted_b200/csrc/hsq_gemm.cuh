@@ -281,12 +281,6 @@ struct GemmCfg {
 template <class Base>
 struct GemmCfgEpi : Base {
   static constexpr bool EPI = true;
-  // Pairs of an operand requested at a time (tokens x outputs tiles).  64 spill a
-  // little next to 128 accumulators.  Measured, 32 and 64: mul 688 and 671 us on groups
-  // of 128 (M = 8192, K = 4096, N = 12288, 603 us without), where 64 spills 16 bytes;
-  // tanh gelu 92 and 96 us on groups of 64 (M = 4096, K = 1152, N = 4608, 83 us without),
-  // where it spills 200.
-  static constexpr int EPI_AHEAD = Base::PRE && Base::BPG == 2 ? 64 : 32;
 };
 
 // Unpack 16 packed bytes (32 codes) into two 16-byte int8 core-matrix rows
@@ -1360,23 +1354,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       }
       // the accumulators already hold U L2 + b (added by the tile's first unit)
       if constexpr (Cfg::TMA_STORE && Cfg::EPI) {
-        // on the accumulators in place; rows and columns outside Y read the last row
-        // and the slice's first columns (the TMA unit clips them)
-        const int live = args.N - (tc * BN + h * CW);
-        size_t mrow[4], rrow[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int m = min(rbase + 8 * i, args.M - 1);
-          int mr = m;
-          if (args.epi.mul_rows != 1) mr = m / args.epi.mul_rows;
-          mrow[i] = static_cast<size_t>(mr) * args.epi.mul_ld + col0;
-          rrow[i] = static_cast<size_t>(m) * args.epi.res_ld + col0;
-        }
-        if (live > 0)
-          epi_apply_quads<4, NBLK, Cfg::EPI_AHEAD>(
-              args.epi, [&](int i, int b) -> float2& { return acc2[i * NBLK + b]; },
-              [&](int i, int b) { return mrow[i] + (8 * b < live ? 8 * b : 0); },
-              [&](int i, int b) { return rrow[i] + (8 * b < live ? 8 * b : 0); });
+        static_assert(CW == 128, "epi_apply");
+        if (tc * BN + h * CW < args.N)
+          epi_apply(args.epi, ystage + dw * 4096, tr * TILE_M + static_cast<int>(crank) * BM + q * 32, tc * BN + h * CW,
+                    args.M, args.N, EpiQuads<NBLK>{acc2});
       }
       if constexpr (Cfg::TMA_STORE) {
         // Stage 32 rows x 128 bytes at a time in this warp's buffer, in the
