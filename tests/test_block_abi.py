@@ -197,3 +197,11 @@ def test_struct_layouts_match_the_header(tmp_path):
         want.append(ctypes.sizeof(c))
         want += [getattr(c, f).offset for f, _ in c._fields_]
     assert got == want
+    # ... and what the two calls pack themselves
+    packed = {hsq._HEADS: hsq._CHeads, hsq._POSITIONS: hsq._CPositions, hsq._PAGED_CACHE: hsq._CPagedCache,
+              hsq._SEQUENCES: hsq._CSequences}
+    for st, c in packed.items():
+        assert st.size == ctypes.sizeof(c)
+        n = len(c._fields_)
+        got = c.from_buffer_copy(st.pack(*range(1, n + 1)))
+        assert [getattr(got, f) for f, _ in c._fields_] == list(range(1, n + 1))

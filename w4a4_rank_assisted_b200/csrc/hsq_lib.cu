@@ -846,30 +846,52 @@ int piece_width(hsq_dtype t, int dim, int pairs, uintptr_t bits) {
   return 1;
 }
 
-// Threads that share the heads of a (token, unit): enough of them for about 1024
-// threads per SM, each with at least one head.
-void split_heads(long long tokens, int units, int heads, int& splits, int& per_split) {
-  const long long want = 1024ll * device_sm_count(), have = tokens * units;
-  long long s = (want + have - 1) / have;
-  s = std::max(1ll, std::min<long long>(s, heads));
-  per_split = static_cast<int>((heads + s - 1) / s);
-  splits = (heads + per_split - 1) / per_split;
+// Blocks of the head kernels per SM before a block takes a second pass.  Measured at
+// 3 (one resident wave) / 18 / one pass each: 4608 tokens x 48 heads x 128 in bf16 22.6 /
+// 20.7 / 25.5 us, 15606 x 16 x 80 in fp32 32.5 / 28.7 / 34.2, the append of 9203 tokens (32 +
+// 8 + 8 heads) 48.6 / 43.4 / 63.7.
+#ifndef HSQ_ROPE_BLOCKS
+#define HSQ_ROPE_BLOCKS 18
+#endif
+// Blocks of a call over `heads` heads of `units` pieces each, `pairs` angles a token:
+// every head of a token in one block where that fits, and as many tokens as then do.
+hsq::RopeGrid rope_grid(int tokens, int units, int heads, int pairs) {
+  hsq::RopeGrid g{};
+  g.units = units;
+  g.lanes = std::min(units, hsq::kRopeThreads);
+  const int slots = hsq::kRopeThreads / g.lanes;
+  g.splits = std::min(slots, (heads + hsq::kRopeHeads - 1) / hsq::kRopeHeads);
+  const int most = hsq::kRopeShared / static_cast<int>(pairs * sizeof(float2) + sizeof(hsq::AppendToken));
+  g.tokens = std::max(1, std::min(slots / g.splits, most));
+  // many tokens: several passes to a block, whose angles and page lookups are formed
+  // at once in front of the first
+  const int full = HSQ_ROPE_BLOCKS * device_sm_count(),
+            rows = (heads + g.splits * hsq::kRopeHeads - 1) / (g.splits * hsq::kRopeHeads);
+  const long long blocks = (tokens + static_cast<long long>(g.tokens) - 1) / g.tokens * rows;
+  g.passes = static_cast<int>(std::max(1ll, std::min<long long>((blocks + full - 1) / full, most / g.tokens)));
+  return g;
+}
+
+template <class Args>
+cudaError_t launch_heads(void (*kernel)(Args), const Args& a, int heads, size_t smem, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>((a.tokens + static_cast<long long>(a.g.tokens) * a.g.passes - 1) / (a.g.tokens * a.g.passes)),
+                  static_cast<unsigned>((heads + a.g.splits * hsq::kRopeHeads - 1) / (a.g.splits * hsq::kRopeHeads)));
+  const int threads = (a.g.lanes * a.g.splits * a.g.tokens + 31) / 32 * 32;
+  return launch_pdl(true, kernel, grid, dim3(threads), smem, st, a);
 }
 
 template <typename T, int V>
 cudaError_t launch_rope(const hsq::RopeArgs& a, bool adjacent, cudaStream_t st) {
-  const long long n = static_cast<long long>(a.tokens) * a.splits * a.units;
-  const dim3 grid(static_cast<unsigned>((n + hsq::kRopeThreads - 1) / hsq::kRopeThreads));
-  return launch_pdl(true, adjacent ? hsq::rope_kernel<T, V, true> : hsq::rope_kernel<T, V, false>, grid,
-                    dim3(hsq::kRopeThreads), 0, st, a);
+  return launch_heads(adjacent ? hsq::rope_kernel<T, V, true> : hsq::rope_kernel<T, V, false>, a, a.heads,
+                      static_cast<size_t>(a.g.tokens) * a.g.passes * a.rot.pairs * sizeof(float2), st);
 }
 
 template <typename T, typename C, int V>
 cudaError_t launch_append(const hsq::AppendArgs& a, bool adjacent, cudaStream_t st) {
-  const long long n = static_cast<long long>(a.tokens) * a.splits * a.units;
-  const dim3 grid(static_cast<unsigned>((n + hsq::kRopeThreads - 1) / hsq::kRopeThreads));
-  return launch_pdl(true, adjacent ? hsq::kv_append_kernel<T, C, V, true> : hsq::kv_append_kernel<T, C, V, false>, grid,
-                    dim3(hsq::kRopeThreads), 0, st, a);
+  return launch_heads(adjacent ? hsq::kv_append_kernel<T, C, V, true> : hsq::kv_append_kernel<T, C, V, false>, a,
+                      a.q_heads + 2 * a.kv_heads,
+                      static_cast<size_t>(a.g.tokens) * a.g.passes *
+                          (a.rot.pairs * sizeof(float2) + sizeof(hsq::AppendToken)), st);
 }
 
 template <typename T, int V>
@@ -1688,9 +1710,7 @@ hsq_status hsq_rope(const hsq_heads* x, const hsq_heads* y, hsq_dtype dtype, int
   a.tokens = tokens; a.heads = heads; a.dim = head_dim;
   const uintptr_t bits = view_bits(*x, tokens, heads, es) | view_bits(*y, tokens, heads, es);
   const int v = piece_width(dtype, head_dim, rot->pairs, bits);
-  a.units = rot->pairs / v + (in_place ? 0 : (head_dim - 2 * rot->pairs) / v);
-  split_heads(tokens, a.units, heads, a.splits, a.per_split);
-  if (static_cast<long long>(tokens) * a.splits * a.units > (1ll << 38)) return HSQ_ERR_UNSUPPORTED;
+  a.g = rope_grid(tokens, rot->pairs / v + (in_place ? 0 : (head_dim - 2 * rot->pairs) / v), heads, rot->pairs);
   const bool adj = rot->interleaved != 0;
   cudaError_t e;
   if (dtype == HSQ_BF16)
@@ -1811,9 +1831,7 @@ hsq_status hsq_kv_append(const hsq_heads* k, const hsq_heads* v, const hsq_heads
   a.q_in_place = in_place ? 1 : 0;
   const int pairs = rot ? rot->pairs : 0;
   const int w = piece_width(dtype, head_dim, pairs, bits);
-  a.units = pairs / w + (head_dim - 2 * pairs) / w;
-  split_heads(tokens, a.units, q_heads + 2 * kv_heads, a.splits, a.per_split);
-  if (static_cast<long long>(tokens) * a.splits * a.units > (1ll << 38)) return HSQ_ERR_UNSUPPORTED;
+  a.g = rope_grid(tokens, pairs / w + (head_dim - 2 * pairs) / w, q_heads + 2 * kv_heads, pairs);
   const bool adj = rot && rot->interleaved;
   cudaError_t e;
   if (dtype == HSQ_BF16)

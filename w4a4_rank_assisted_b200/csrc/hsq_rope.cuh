@@ -5,9 +5,18 @@
 // along the pair's axis is p turns by t = p f_i:
 //     (x, y) -> scale (x cos t - y sin t, x sin t + y cos t);
 // with t -> -t the map is the transpose, which is its gradient.  Both kernels move
-// bytes: every element is read and written once, and the angle is shared by all
-// heads of a token, so a thread keeps the angles of V pairs (two pieces of V
-// elements) in registers and walks over heads with them.
+// bytes: every element is read and written once, and the angles are shared by all
+// heads of a token.  A block takes a few tokens with all their heads (as many as fit):
+// it forms each token's angles once, into shared memory, while the first pieces that
+// its threads have requested are on their way; then every thread rotates its pieces of
+// two heads, pass by pass, the next pass's pieces requested first.  (A thread that
+// formed its own angles and walked over the heads took twice as long.)
+//
+// Bound by memory once there are enough tokens: 20.7 us at 4608 tokens x 48 heads x 128
+// in bf16 (113 MB: 5.5 TB/s, 0.84 of the copy rate), 27 us at 15606 x 16 x 80 in fp32 (160
+// MB: 0.9), 43 us for the append of 9203 tokens of 32 + 8 + 8 heads x 128 (226 MB: 0.8);
+// by launch and latency below: 2.3 us for one token's rotation, 3.2 us for its append
+// (a page lookup is three loads that depend on one another).
 //
 // The angle: p f_i is formed in fp64 (a product of 24-bit factors is exact there;
 // in fp32, position 10^5 leaves an angle an error of 4e-3), divided by 2 pi, its
@@ -20,9 +29,11 @@
 namespace hsq {
 
 constexpr int kRopeMaxPairs = 256;
-constexpr int kRopeThreads = 256;
-// heads whose pieces a thread requests before it uses the first
-constexpr int kRopeBatch = 4;
+constexpr int kRopeThreads = 256;  // most threads of a block
+// Heads of a thread and a pass.  Four hold 16 more registers a piece: at two blocks per
+// SM instead of three 23.5 against 20.7 us (4608 tokens x 48 heads x 128, bf16).
+constexpr int kRopeHeads = 2;
+constexpr int kRopeShared = 32768;  // shared memory of a block's tokens: their angles and cache rows
 
 enum PosType { kPosI32 = 0, kPosI64 = 1, kPosF32 = 2 };
 enum HeadType { kHeadBf16 = 0, kHeadF32 = 1, kHeadE4m3 = 2 };
@@ -61,24 +72,25 @@ __device__ __forceinline__ void rope_angle(const RopeTable& t, int i, size_t row
   s *= t.scale * t.sign;
 }
 
-// V consecutive elements of a head as fp32, and back.
+// V consecutive elements of a head as loaded (one access), and as fp32.
 template <typename T, int V>
-__device__ __forceinline__ void load_piece(const T* p, float (&f)[V]) {
-  if constexpr (sizeof(T) == 2 && V == 8) {
-    bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), f);
-  } else if constexpr (sizeof(T) == 2 && V == 4) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
-    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-    f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
-  } else if constexpr (sizeof(T) == 4 && V == 4) {
-    const float4 w = *reinterpret_cast<const float4*>(p);
-    f[0] = w.x; f[1] = w.y; f[2] = w.z; f[3] = w.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = static_cast<float>(p[j]);
+struct Piece {
+  uint32_t w[V * sizeof(T) / 4];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (sizeof(w) == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
   }
-}
+  __device__ __forceinline__ float at(int j) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+    else return __uint_as_float((j & 1) ? (w[j / 2] & 0xffff0000u) : (w[j / 2] << 16));
+  }
+};
+template <typename T>
+struct Piece<T, 1> {
+  T x;
+  __device__ __forceinline__ void load(const T* p) { x = *p; }
+  __device__ __forceinline__ float at(int) const { return static_cast<float>(x); }
+};
 
 // Two values -> two E4M3 bytes (the first in the low byte): nearest, ties to
 // even, saturating at 448; NaN stays NaN.
@@ -159,72 +171,118 @@ struct RopeUnit {
   __device__ __forceinline__ int pair(int j) const {
     return (ADJ && V > 1) ? (j < V / 2 ? pa + j : pb + j - V / 2) : pa + j;
   }
-  static __device__ __forceinline__ void rotate(float (&x)[V], float (&y)[V], const float (&c)[V], const float (&s)[V]) {
-    auto turn = [](float& p, float& q, float cc, float ss) {
-      const float p0 = p;
-      p = fmaf(p0, cc, -q * ss);
-      q = fmaf(p0, ss, q * cc);
-    };
-    if constexpr (ADJ && V > 1) {
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        turn(x[2 * j], x[2 * j + 1], c[j], s[j]);
-        turn(y[2 * j], y[2 * j + 1], c[V / 2 + j], s[V / 2 + j]);
-      }
+  // the pieces (p, q) turned by the angles (c, s): x and y of pair j are gathered, two
+  // pairs a packed instruction
+  static __device__ __forceinline__ void rotate(float (&p)[V], float (&q)[V], const float (&c)[V], const float (&s)[V]) {
+    auto x = [&](int j) -> float& { return (ADJ && V > 1) ? (j < V / 2 ? p[2 * j] : q[2 * j - V]) : p[j]; };
+    auto y = [&](int j) -> float& { return (ADJ && V > 1) ? (j < V / 2 ? p[2 * j + 1] : q[2 * j + 1 - V]) : q[j]; };
+    if constexpr (V == 1) {
+      const float x0 = p[0];
+      p[0] = fmaf(x0, c[0], q[0] * -s[0]);
+      q[0] = fmaf(x0, s[0], q[0] * c[0]);
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) turn(x[j], y[j], c[j], s[j]);
+      for (int j = 0; j < V; j += 2) {
+        const float2 xx = make_float2(x(j), x(j + 1)), yy = make_float2(y(j), y(j + 1));
+        const float2 cc = make_float2(c[j], c[j + 1]), ss = make_float2(s[j], s[j + 1]);
+        const float2 u = __ffma2_rn(xx, cc, __fmul2_rn(yy, make_float2(-ss.x, -ss.y)));
+        const float2 v = __ffma2_rn(xx, ss, __fmul2_rn(yy, cc));
+        x(j) = u.x; x(j + 1) = u.y;
+        y(j) = v.x; y(j + 1) = v.y;
+      }
     }
   }
+};
+
+// How a call is cut into blocks: a block takes `passes` times `tokens` tokens and
+// `splits` x kRopeHeads heads, its threads (token, split, unit) with the units fastest
+// (neighbours read neighbouring pieces of a head); grid (token blocks, head blocks).
+// A head of more than kRopeThreads units is walked over.
+struct RopeGrid {
+  int units, lanes;  // pieces to walk, threads on them
+  int splits, tokens, passes;
 };
 
 struct RopeArgs {
   HeadsView x, y;
   RopeTable rot;
+  RopeGrid g;
   int tokens, heads, dim;
-  int units;      // of a head: P / V, and the unrotated pieces unless x is y
-  int splits;     // threads that share a (token, unit)'s heads
-  int per_split;  // heads of each
 };
 
-// Thread (token, split, unit), units fastest: neighbours read neighbouring
-// pieces of one head.
 template <typename T, int V, bool ADJ>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 4 : 3) rope_kernel(const __grid_constant__ RopeArgs a) {
+  extern __shared__ float2 rope_angles[];  // [tokens of the block][pairs]
   grid_dep_wait();  // x comes from the preceding kernel
   if (threadIdx.x == 0) grid_dep_launch();
-  const long long idx = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
-  const long long row = idx / a.units;
-  const int u = static_cast<int>(idx - row * a.units);
-  const long long tok = row / a.splits;
-  if (tok >= a.tokens) return;
-  const int h0 = static_cast<int>(row - tok * a.splits) * a.per_split, h1 = min(a.heads, h0 + a.per_split);
-  const RopeUnit<V, ADJ> un(u, a.rot.pairs);
-  const T* x = static_cast<const T*>(a.x.data) + tok * a.x.ts;
-  T* y = static_cast<T*>(a.y.data) + tok * a.y.ts;
-  float c[V], s[V];
-  if (un.b >= 0) {
+  const int t = threadIdx.x, P = a.rot.pairs;
+  const int u0 = t % a.g.lanes, slot = t / a.g.lanes, sp = slot % a.g.splits, tk = slot / a.g.splits;
+  const int t0 = static_cast<int>(blockIdx.x) * a.g.tokens * a.g.passes;  // (below tokens)
+  const int n = min(a.g.tokens * a.g.passes, a.tokens - t0);              // tokens of the block
+  const int h0 = (static_cast<int>(blockIdx.y) * a.g.splits + sp) * kRopeHeads;
+  // out of range: the block's last token and the last head are read, and nothing is written
+  const T* x = static_cast<const T*>(a.x.data) + static_cast<long long>(t0) * a.x.ts;
+  T* y = static_cast<T*>(a.y.data) + static_cast<long long>(t0) * a.y.ts;
+  Piece<T, V> p[kRopeHeads], q[kRopeHeads];
+  auto load = [&](int k, const RopeUnit<V, ADJ>& un) {
+    const T* xk = x + min(k, n - 1) * a.x.ts;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      rope_angle(a.rot, un.pair(j), static_cast<size_t>(tok % a.rot.pos_rows), 0.0, c[j], s[j]);
+    for (int i = 0; i < kRopeHeads; ++i) {
+      const T* xh = xk + min(h0 + i, a.heads - 1) * a.x.hs;
+      p[i].load(xh + un.a);
+      q[i].load(xh + (un.b < 0 ? un.a : un.b));
+    }
+  };
+  load(tk, RopeUnit<V, ADJ>(u0, P));
+  for (int i = t; i < n * P; i += blockDim.x) {
+    const int k = i / P, j = i - k * P;
+    float c, s;
+    rope_angle(a.rot, j, static_cast<size_t>((t0 + k) % a.rot.pos_rows), 0.0, c, s);
+    rope_angles[i] = make_float2(c, s);
   }
-  for (int h = h0; h < h1; h += kRopeBatch) {
-    float p[kRopeBatch][V], q[kRopeBatch][V];
+  __syncthreads();
+  if (tk >= a.g.tokens || h0 >= a.heads) return;
+  const int walk = (a.g.units - u0 + a.g.lanes - 1) / a.g.lanes;  // units of this thread
+  for (int k = tk, w = 0; k < n;) {
+    const float2* ang = rope_angles + k * P;
+    T* yk = y + k * a.y.ts;
+    const RopeUnit<V, ADJ> un(u0 + w * a.g.lanes, P);
+    Piece<T, V> pc[kRopeHeads], qc[kRopeHeads];
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i)
-      if (h + i < h1) {
-        load_piece<T, V>(x + (h + i) * a.x.hs + un.a, p[i]);
-        if (un.b >= 0) load_piece<T, V>(x + (h + i) * a.x.hs + un.b, q[i]);
-      }
+    for (int i = 0; i < kRopeHeads; ++i) {
+      pc[i] = p[i];
+      qc[i] = q[i];
+    }
+    if (++w == walk) {
+      w = 0;
+      k += a.g.tokens;
+    }
+    if (k < n) load(k, RopeUnit<V, ADJ>(u0 + w * a.g.lanes, P));  // the next pass's pieces
+    float c[V], s[V];
+    if (un.b >= 0) {
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i)
-      if (h + i < h1) {
-        if (un.b >= 0) {
-          RopeUnit<V, ADJ>::rotate(p[i], q[i], c, s);
-          store_piece<V>(y + (h + i) * a.y.hs + un.b, q[i]);
-        }
-        store_piece<V>(y + (h + i) * a.y.hs + un.a, p[i]);
+      for (int j = 0; j < V; ++j) {
+        const float2 cs = ang[un.pair(j)];
+        c[j] = cs.x;
+        s[j] = cs.y;
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kRopeHeads; ++i) {
+      if (h0 + i >= a.heads) break;
+      T* yh = yk + (h0 + i) * a.y.hs;
+      float f[V], g[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        f[j] = pc[i].at(j);
+        g[j] = qc[i].at(j);
+      }
+      if (un.b >= 0) {
+        RopeUnit<V, ADJ>::rotate(f, g, c, s);
+        store_piece<V>(yh + un.b, g);
+      }
+      store_piece<V>(yh + un.a, f);
+    }
   }
 }
 
@@ -238,13 +296,13 @@ struct AppendArgs {
   HeadsView k, v, q, q_out;
   CacheView kc, vc;
   RopeTable rot;       // pairs = 0: no rotation
+  RopeGrid g;          // over the q heads, then the k heads, then the v heads
   const int* table;    // [seqs][table_ld] page of each page_size tokens
   const int* lens;     // [seqs] tokens already cached; negative: the sequence takes no part
   const int* cu;       // [seqs + 1], or nullptr: token t is sequence t's
   long long table_ld;
   int tokens, seqs, q_heads, kv_heads, dim;
   int pages, page_size, max_pages;
-  int units, splits, per_split;
   int q_in_place;
 };
 
@@ -271,84 +329,127 @@ __device__ __forceinline__ bool append_place(const AppendArgs& a, int t, int& se
   return true;
 }
 
-// Thread (token, split, unit) as in rope_kernel; its heads are the q heads, then
-// the k heads, then the v heads.  C: the cache's element type.
+// What a block knows of one of its tokens: its place in its sequence (negative: it
+// takes no part), and the cache row it goes to (page < 0: none).
+struct AppendToken {
+  long long pos;
+  int page, slot;
+};
+
+// C: the cache's element type.
 template <typename T, typename C, int V, bool ADJ>
-__global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 3) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+  extern __shared__ float2 rope_angles[];  // [tokens of the block][pairs], then the tokens
+  AppendToken* toks = reinterpret_cast<AppendToken*>(rope_angles + a.g.tokens * a.g.passes * a.rot.pairs);
   grid_dep_wait();
   if (threadIdx.x == 0) grid_dep_launch();
-  const long long idx = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
-  const long long row = idx / a.units;
-  const int u = static_cast<int>(idx - row * a.units);
-  const long long tok = row / a.splits;
-  if (tok >= a.tokens) return;
-  const int nh = a.q_heads + 2 * a.kv_heads;
-  const int h0 = static_cast<int>(row - tok * a.splits) * a.per_split, h1 = min(nh, h0 + a.per_split);
-  const RopeUnit<V, ADJ> un(u, a.rot.pairs);
-  int seq = 0;
-  long long pos = 0;
-  if (!append_place(a, static_cast<int>(tok), seq, pos)) return;
-  // the page: a table entry outside the cache, or a place outside the table, is
-  // reported and nothing is written for the token's k and v
-  const long long pi = pos / a.page_size;
-  int page = -1;
-  if (h1 > a.q_heads) {
-    if (pi < a.max_pages) page = __ldg(a.table + static_cast<long long>(seq) * a.table_ld + pi);
-    if (page < 0 || page >= a.pages) {
-      page = -1;
-      atomicOr(&g_status, kStatusBadPage);
+  const int t = threadIdx.x, P = a.rot.pairs;
+  const int u0 = t % a.g.lanes, slot = t / a.g.lanes, sp = slot % a.g.splits, tk = slot / a.g.splits;
+  const int t0 = static_cast<int>(blockIdx.x) * a.g.tokens * a.g.passes;  // (below tokens)
+  const int n = min(a.g.tokens * a.g.passes, a.tokens - t0);              // tokens of the block
+  const int nh = a.q_heads + 2 * a.kv_heads, nr = a.q_heads + a.kv_heads;
+  const int h0 = (static_cast<int>(blockIdx.y) * a.g.splits + sp) * kRopeHeads;
+  Piece<T, V> p[kRopeHeads], q[kRopeHeads];
+  auto load = [&](int k, const RopeUnit<V, ADJ>& un) {
+    const long long tok = t0 + min(k, n - 1);
+#pragma unroll
+    for (int i = 0; i < kRopeHeads; ++i) {
+      const int e = min(h0 + i, nh - 1);
+      const HeadsView& src = e < a.q_heads ? a.q : e < nr ? a.k : a.v;
+      const int hd = e - (e < a.q_heads ? 0 : e < nr ? a.q_heads : nr);
+      const T* x = static_cast<const T*>(src.data) + tok * src.ts + hd * src.hs;
+      p[i].load(x + un.a);
+      q[i].load(x + (un.b < 0 ? un.a : un.b));
     }
-  }
-  const long long slot = pos - pi * a.page_size;
-  float c[V], s[V];
-  if (un.b >= 0 && h0 < a.q_heads + a.kv_heads) {
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      rope_angle(a.rot, un.pair(j), static_cast<size_t>(tok), static_cast<double>(pos), c[j], s[j]);
-  }
-  const T* xq = static_cast<const T*>(a.q.data) + tok * a.q.ts;
-  const T* xk = static_cast<const T*>(a.k.data) + tok * a.k.ts;
-  const T* xv = static_cast<const T*>(a.v.data) + tok * a.v.ts;
-  for (int h = h0; h < h1; h += kRopeBatch) {
-    float p[kRopeBatch][V], q[kRopeBatch][V];
-#pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i)
-      if (h + i < h1) {
-        const int e = h + i;
-        const T* x = e < a.q_heads ? xq + e * a.q.hs
-                     : e < a.q_heads + a.kv_heads ? xk + (e - a.q_heads) * a.k.hs
-                                                  : xv + (e - a.q_heads - a.kv_heads) * a.v.hs;
-        load_piece<T, V>(x + un.a, p[i]);
-        if (un.b >= 0) load_piece<T, V>(x + un.b, q[i]);
+  };
+  load(tk, RopeUnit<V, ADJ>(u0, P));
+  for (int k = t; k < n; k += blockDim.x) {
+    AppendToken o{-1, -1, 0};
+    int seq = 0;
+    if (append_place(a, t0 + k, seq, o.pos)) {
+      // the page: a table entry outside the cache, or a place outside the table, is
+      // reported and nothing is written for the token's k and v
+      const long long pi = o.pos >> 32 ? o.pos / a.page_size
+                                       : static_cast<long long>(static_cast<uint32_t>(o.pos) / static_cast<uint32_t>(a.page_size));
+      if (pi < a.max_pages) o.page = __ldg(a.table + static_cast<long long>(seq) * a.table_ld + pi);
+      if (o.page < 0 || o.page >= a.pages) {
+        o.page = -1;
+        atomicOr(&g_status, kStatusBadPage);
       }
+      o.slot = static_cast<int>(o.pos - pi * a.page_size);
+    }
+    toks[k] = o;
+  }
+  __syncthreads();
+  for (int i = t; i < n * P; i += blockDim.x) {
+    const int k = i / P, j = i - k * P;
+    float c, s;
+    rope_angle(a.rot, j, static_cast<size_t>(t0 + k), static_cast<double>(toks[k].pos), c, s);
+    rope_angles[i] = make_float2(c, s);
+  }
+  __syncthreads();
+  if (tk >= a.g.tokens || h0 >= nh) return;
+  const int walk = (a.g.units - u0 + a.g.lanes - 1) / a.g.lanes;  // units of this thread
+  for (int k = tk, w = 0; k < n;) {
+    const AppendToken me = toks[k];
+    const long long tok = t0 + k;
+    const float2* ang = rope_angles + k * P;
+    const RopeUnit<V, ADJ> un(u0 + w * a.g.lanes, P);
+    Piece<T, V> pc[kRopeHeads], qc[kRopeHeads];
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i)
-      if (h + i < h1) {
-        const int e = h + i;
-        if (un.b >= 0 && e < a.q_heads + a.kv_heads) RopeUnit<V, ADJ>::rotate(p[i], q[i], c, s);
-        if (e < a.q_heads) {
-          T* y = static_cast<T*>(a.q_out.data) + tok * a.q_out.ts + e * a.q_out.hs;
-          if (un.b >= 0) store_piece<V>(y + un.b, q[i]);
-          if (un.b >= 0 || !a.q_in_place) store_piece<V>(y + un.a, p[i]);
-        } else if (page >= 0) {
-          const bool is_k = e < a.q_heads + a.kv_heads;
-          const CacheView& cv = is_k ? a.kc : a.vc;
-          const int hd = e - a.q_heads - (is_k ? 0 : a.kv_heads);
-          C* y = static_cast<C*>(cv.data) + page * cv.ps + slot * cv.ss + hd * cv.hs;
-          if constexpr (sizeof(C) == 1) {
-            if (cv.scale) {
-              const float sc = __ldg(cv.scale + hd);
+    for (int i = 0; i < kRopeHeads; ++i) {
+      pc[i] = p[i];
+      qc[i] = q[i];
+    }
+    if (++w == walk) {
+      w = 0;
+      k += a.g.tokens;
+    }
+    if (k < n) load(k, RopeUnit<V, ADJ>(u0 + w * a.g.lanes, P));  // the next pass's pieces
+    if (me.pos < 0) continue;
+    float c[V], s[V];
+    if (un.b >= 0) {
 #pragma unroll
-              for (int j = 0; j < V; ++j) {
-                p[i][j] = __fdiv_rn(p[i][j], sc);
-                if (un.b >= 0) q[i][j] = __fdiv_rn(q[i][j], sc);
-              }
+      for (int j = 0; j < V; ++j) {
+        const float2 cs = ang[un.pair(j)];
+        c[j] = cs.x;
+        s[j] = cs.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRopeHeads; ++i) {
+      const int e = h0 + i;
+      if (e >= nh) break;
+      float f[V], g[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        f[j] = pc[i].at(j);
+        g[j] = qc[i].at(j);
+      }
+      if (un.b >= 0 && e < nr) RopeUnit<V, ADJ>::rotate(f, g, c, s);
+      if (e < a.q_heads) {
+        T* y = static_cast<T*>(a.q_out.data) + tok * a.q_out.ts + e * a.q_out.hs;
+        if (un.b >= 0) store_piece<V>(y + un.b, g);
+        if (un.b >= 0 || !a.q_in_place) store_piece<V>(y + un.a, f);
+      } else if (me.page >= 0) {
+        const bool is_k = e < nr;
+        const CacheView& cv = is_k ? a.kc : a.vc;
+        const int hd = e - (is_k ? a.q_heads : nr);
+        C* y = static_cast<C*>(cv.data) + me.page * cv.ps + me.slot * cv.ss + hd * cv.hs;
+        if constexpr (sizeof(C) == 1) {
+          if (cv.scale) {
+            const float sc = __ldg(cv.scale + hd);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              f[j] = __fdiv_rn(f[j], sc);
+              g[j] = __fdiv_rn(g[j], sc);
             }
           }
-          store_piece<V>(y + un.a, p[i]);
-          if (un.b >= 0) store_piece<V>(y + un.b, q[i]);
         }
+        store_piece<V>(y + un.a, f);
+        if (un.b >= 0) store_piece<V>(y + un.b, g);
       }
+    }
   }
 }
 

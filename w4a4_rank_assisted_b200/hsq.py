@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -182,8 +183,14 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
+#: The current stream's handle without a Stream object around it (3 us a call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -407,43 +414,51 @@ class Rotation:
         self._axes = bytes(axes)
         self._c = _CRotation(freqs=freqs.data_ptr(), pair_axis=self._axes, pairs=self.pairs, n_axes=self.n_axes,
                              interleaved=int(self.interleaved), transpose=int(self.transpose), scale=self.scale)
+        self._ref = ctypes.byref(self._c)
 
 
-def _heads(t: torch.Tensor, name: str, shape=None) -> _CHeads:
+# The structures of the two calls below, packed as C lays them out: a call of a few
+# microseconds does not wait for ctypes to build them.
+_HEADS = struct.Struct("@Pqq")
+_POSITIONS = struct.Struct("@Piiq")
+_PAGED_CACHE = struct.Struct("@PPiiiqqqPP")
+_SEQUENCES = struct.Struct("@PPPiiq")
+
+
+def _heads(t: torch.Tensor, name: str, shape=None) -> bytes:
     if not t.is_cuda:
         raise ValueError("libhsq takes CUDA tensors only")
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    strides = t.stride()
+    if len(strides) != 3 or (strides[2] != 1 and t.shape[2] > 1):
         raise ValueError(f"{name} is [tokens, heads, head_dim] with a dense last dimension")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
-    return _CHeads(t.data_ptr(), t.stride(0), t.stride(1))
+    return _HEADS.pack(t.data_ptr(), strides[0], strides[1])
 
 
-def _positions(p: torch.Tensor, rotation: Rotation) -> _CPositions:
+def _positions(p: torch.Tensor, rotation: Rotation) -> bytes:
     if not p.is_cuda:
         raise ValueError("libhsq takes CUDA tensors only")
-    if p.dtype not in _POS_DTYPES:
+    kind = _POS_DTYPES.get(p.dtype)
+    if kind is None:
         raise ValueError(f"positions are int32, int64 or float32, not {p.dtype}")
-    if p.dim() == 1:
-        p = p[:, None]
-    if p.dim() != 2 or p.shape[1] != rotation.n_axes or (p.shape[1] > 1 and p.stride(1) != 1):
+    shape, strides = p.shape, p.stride()
+    rows, axes = (shape[0], 1) if len(shape) == 1 else (shape[0], shape[1]) if len(shape) == 2 else (0, 0)
+    if axes != rotation.n_axes or (axes > 1 and strides[1] != 1):
         raise ValueError(f"positions are [rows, {rotation.n_axes}] with a dense last dimension")
-    return _CPositions(p.data_ptr(), _POS_DTYPES[p.dtype], p.shape[0],
-                       p.stride(0) if p.shape[0] > 1 else p.shape[1])
+    return _POSITIONS.pack(p.data_ptr(), kind, rows, strides[0] if rows > 1 else axes)
 
 
-def _one_device(*tensors) -> torch.device:
-    dev = tensors[0].device
-    for t in tensors[1:]:
-        if t is not None and t.device != dev:
+def _same_device(index: int, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.get_device() != index:
             raise ValueError("the call's tensors live on different devices")
-    return dev
 
 
-def _on_device(dev: torch.device, stream, call):
-    """call(stream) with the tensors' device current; stream None: its current stream."""
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
+def _on_device(index: int, stream, call):
+    """call(stream) with device `index` current; stream None: that device's current stream."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
             return call(_stream(stream))
     return call(_stream(stream))
 
@@ -452,16 +467,17 @@ def hsq_rope(x: torch.Tensor, y: torch.Tensor, positions: torch.Tensor, rotation
     """y = x rotated by its positions: x and y [tokens, heads, head_dim] (any token
     and head strides; y may be x), positions [rows] or [rows, axes], token t taking
     row t % rows.  With rotation.transpose the gradient of that map."""
-    h = _heads(x, "x")
-    if x.dtype not in _HEAD_DTYPES or y.dtype != x.dtype:
+    kind = _HEAD_DTYPES.get(x.dtype)
+    if kind is None or y.dtype != x.dtype:
         raise ValueError("x and y are both bfloat16 or both float32")
-    hy = _heads(y, "y", x.shape)
-    T, H, D = x.shape
+    shape = x.shape
+    hx = _heads(x, "x")
+    hy = hx if y is x else _heads(y, "y", shape)
     pos = _positions(positions, rotation)
-    dev = _one_device(x, y, positions, rotation.freqs)
-    ref = ctypes.byref
-    _check(_on_device(dev, stream, lambda s: load().hsq_rope(
-        ref(h), ref(hy), _HEAD_DTYPES[x.dtype], T, H, D, ref(rotation._c), ref(pos), s)), "hsq_rope")
+    index = x.get_device()
+    _same_device(index, y, positions, rotation.freqs)
+    _check(_on_device(index, stream, lambda s: load().hsq_rope(
+        hx, hy, kind, shape[0], shape[1], shape[2], rotation._ref, pos, s)), "hsq_rope")
 
 
 def hsq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -476,10 +492,12 @@ def hsq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cac
     q_out.  block_table int32 [sequences, max_pages], cache_lens int32
     [sequences], cu_seqlens int32 [sequences + 1] or None for one token per
     sequence.  See include/hsq.h."""
-    if k.dtype not in _HEAD_DTYPES or v.dtype != k.dtype:
+    kind = _HEAD_DTYPES.get(k.dtype)
+    if kind is None or v.dtype != k.dtype:
         raise ValueError("k and v are both bfloat16 or both float32")
-    hk, hv = _heads(k, "k"), _heads(v, "v", k.shape)
-    T, H, D = k.shape
+    shape = k.shape
+    hk, hv = _heads(k, "k"), _heads(v, "v", shape)
+    T, H, D = shape
     hq = hqo = None
     q_heads = 0
     if (q is None) != (q_out is None):
@@ -487,45 +505,53 @@ def hsq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cac
     if q is not None:
         if q.dtype != k.dtype or q_out.dtype != k.dtype:
             raise ValueError("q, q_out and k have one type")
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.shape[1] < 1:
-            raise ValueError(f"q is {tuple(q.shape)}, k is {tuple(k.shape)}")
-        hq, hqo = _heads(q, "q"), _heads(q_out, "q_out", q.shape)
-        q_heads = q.shape[1]
-    if k_cache.dtype not in _CACHE_DTYPES or v_cache.dtype != k_cache.dtype:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != D or q_shape[1] < 1:
+            raise ValueError(f"q is {tuple(q_shape)}, k is {tuple(shape)}")
+        hq, hqo = _heads(q, "q"), _heads(q_out, "q_out", q_shape)
+        q_heads = q_shape[1]
+    cache_kind = _CACHE_DTYPES.get(k_cache.dtype)
+    if cache_kind is None or v_cache.dtype != k_cache.dtype:
         raise ValueError("the caches are both bfloat16, float32 or float8_e4m3fn")
-    if k_cache.dim() != 4 or k_cache.shape[2:] != k.shape[1:] or v_cache.shape != k_cache.shape:
+    c_shape, c_strides = k_cache.shape, k_cache.stride()
+    if len(c_shape) != 4 or c_shape[2:] != shape[1:] or v_cache.shape != c_shape:
         raise ValueError(f"the caches are [pages, page_size, {H}, {D}], both")
-    if v_cache.stride() != k_cache.stride() or (D > 1 and k_cache.stride(3) != 1):
+    if v_cache.stride() != c_strides or (D > 1 and c_strides[3] != 1):
         raise ValueError("the caches have equal strides and a dense last dimension")
-    ints = [("block_table", block_table, 2), ("cache_lens", cache_lens, 1)]
+    B = cache_lens.shape[0] if cache_lens.dim() == 1 else -1
+    t_shape, t_strides = block_table.shape, block_table.stride()
+    if block_table.dtype != torch.int32 or len(t_shape) != 2 or t_shape[0] != B or \
+            (t_shape[1] > 1 and t_strides[1] != 1):
+        raise ValueError("block_table is int32 [sequences, max_pages], dense in the last dimension")
+    if cache_lens.dtype != torch.int32 or not cache_lens.is_contiguous():
+        raise ValueError("cache_lens is a contiguous int32 vector")
+    cu = 0
     if cu_seqlens is not None:
-        ints.append(("cu_seqlens", cu_seqlens, 1))
-    for name, t, dims in ints:
-        if t.dtype != torch.int32 or t.dim() != dims or (t.numel() > 1 and t.shape[-1] > 1 and t.stride(-1) != 1):
-            raise ValueError(f"{name} is an int32 tensor of {dims} dimension(s), dense in the last")
-    B = cache_lens.shape[0]
-    if block_table.shape[0] != B or (cu_seqlens is not None and cu_seqlens.shape[0] != B + 1):
-        raise ValueError(f"{B} sequences, block_table {tuple(block_table.shape)}"
-                         + ("" if cu_seqlens is None else f", cu_seqlens {tuple(cu_seqlens.shape)}"))
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (H,) or not t.is_contiguous()):
-            raise ValueError(f"{name} is float32 [{H}]")
-    if positions is not None and rotation is None:
+        if cu_seqlens.dtype != torch.int32 or tuple(cu_seqlens.shape) != (B + 1,) or not cu_seqlens.is_contiguous():
+            raise ValueError(f"cu_seqlens is a contiguous int32 [{B + 1}]")
+        cu = cu_seqlens.data_ptr()
+    scales = [0, 0]
+    for i, t in enumerate((k_scale, v_scale)):
+        if t is not None:
+            if t.dtype != torch.float32 or tuple(t.shape) != (H,) or not t.is_contiguous():
+                raise ValueError(f"k_scale and v_scale are float32 [{H}]")
+            scales[i] = t.data_ptr()
+    rot = pos = None
+    index = k.get_device()
+    if rotation is not None:
+        rot = rotation._ref
+        _same_device(index, rotation.freqs)
+        if positions is not None:
+            pos = _positions(positions, rotation)
+    elif positions is not None:
         raise ValueError("positions without a rotation")
-    pos = None if positions is None else _positions(positions, rotation)
-    dev = _one_device(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens, positions, q, q_out, k_scale,
-                      v_scale, None if rotation is None else rotation.freqs)
-    opt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    cache = _CPagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _CACHE_DTYPES[k_cache.dtype], k_cache.shape[0],
-                         k_cache.shape[1], k_cache.stride(0), k_cache.stride(1), k_cache.stride(2), opt(k_scale),
-                         opt(v_scale))
-    seqs = _CSequences(block_table.data_ptr(), cache_lens.data_ptr(), opt(cu_seqlens), B, block_table.shape[1],
-                       block_table.stride(0) if B > 1 else block_table.shape[1])
-    ref = lambda c: None if c is None else ctypes.byref(c)  # noqa: E731
-    _check(_on_device(dev, stream, lambda s: load().hsq_kv_append(
-        ref(hk), ref(hv), ref(hq), ref(hqo), _HEAD_DTYPES[k.dtype], T, q_heads, H, D,
-        None if rotation is None else ctypes.byref(rotation._c), ref(pos), ref(cache), ref(seqs), s)),
-        "hsq_kv_append")
+    _same_device(index, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens, positions, q, q_out, k_scale, v_scale)
+    cache = _PAGED_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), cache_kind, c_shape[0], c_shape[1], c_strides[0],
+                              c_strides[1], c_strides[2], scales[0], scales[1])
+    seqs = _SEQUENCES.pack(block_table.data_ptr(), cache_lens.data_ptr(), cu, B, t_shape[1],
+                           t_strides[0] if B > 1 else t_shape[1])
+    _check(_on_device(index, stream, lambda s: load().hsq_kv_append(
+        hk, hv, hq, hqo, kind, T, q_heads, H, D, rot, pos, cache, seqs, s)), "hsq_kv_append")
 
 
 def _sm_count() -> int:
