@@ -295,7 +295,9 @@ hsq_status hsq_linear_forward_fused(const void* X_bf16, const float* s, const vo
  * their row strides are multiples of 8 (HSQ_ERR_UNSUPPORTED otherwise) and at
  * least N.  residual may be Y itself (the same pointer and type, stride N), and so
  * may mul with mul_rows = 1; an operand that overlaps Y in any other way is
- * refused (HSQ_ERR_INVALID_ARG).  A NULL epilogue, or one that asks for nothing,
+ * refused (HSQ_ERR_INVALID_ARG).  Y, and with it residual, may also be X in
+ * hsq_linear_forward_x_ep (N == K); hsq_linear_forward_fused_ep refuses a Y that
+ * overlaps X, which its blocks read while others write Y.  A NULL epilogue, or one that asks for nothing,
  * is the forward without it, bit for bit.
  * The paper has no counterpart: in a transformer block these steps follow the
  * linear's output elementwise.

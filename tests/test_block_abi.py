@@ -59,6 +59,14 @@ def test_epilogue_refusals(form):
     assert f(_epilogue(mul=A - 128, mul_rows=16, mul_ld=64, residual=A + 2048 - 16)) == INVALID
 
 
+def test_fused_epilogue_refuses_y_over_x():
+    lib = hsq.load()
+    far = 1 << 30
+    call = lambda X, Y: lib.hsq_linear_forward_fused_ep(X, far, far, far, far, far, None, 16, 64, 64, 4, 64, Y, 0,  # noqa: E731
+                                                        _epilogue(), None)
+    assert call(A, A) == INVALID and call(A, A + 1024) == INVALID
+
+
 def test_epilogue_object_checks():
     with pytest.raises(ValueError):
         hsq.Epilogue("swish")

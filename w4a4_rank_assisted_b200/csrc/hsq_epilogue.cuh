@@ -192,9 +192,9 @@ __device__ __forceinline__ float2 epi_pair16(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// How the threads hold the warp's accumulators of 32 rows and 128 columns, and read a
+// How the threads hold the warp's accumulators of 32 rows, and read a
 // box for them: use16 / use32 apply f(z, operand) to the pairs of neighbouring
-// columns in a box of 32 bf16 / 16 fp32 columns, the k-th of the 128.
+// columns in a box of 32 bf16 / 16 fp32 columns, the k-th of the warp's.
 //   Quads: tcgen05.ld 16x256b: lane l has rows l / 4 + 8i and columns 8b + 2 (l % 4), + 1
 template <int NBLK>
 struct EpiQuads {
@@ -262,7 +262,7 @@ struct EpiRows {
   }
 };
 
-// act(z) * mul + residual in place on the warp's accumulators of 32 rows y0 .. and 128
+// act(z) * mul + residual in place on the warp's accumulators of 32 rows y0 .. and CW
 // columns n0 .. (n0 < N).  stg: the warp's 4 KB staging buffer, through which the
 // operands come in two boxes of 2 KB in turn, each requested while the one before it is
 // used, the first two ahead of the activation.
@@ -279,11 +279,11 @@ struct EpiRows {
 // 1152, N = 4608, groups of 64; NVFP4 at M = 4096, K = 4608, N = 1152: 95.8 / 98.7 / 99.6 /
 // 100.7 / 104.9.  (A pass of its own over Y and mul reads and writes 600 MB at the
 // first size: 92 us.)
-template <class Acc>
+template <int CW, class Acc>
 __device__ __forceinline__ void epi_apply(const EpiArgs& e, uint8_t* stg, int y0, int n0, int M, int N, Acc&& acc) {
   const EpiOperand mul{e.mul, e.mul_ld, e.mul_rows, e.mul_f32 != 0}, res{e.res, e.res_ld, 1, e.res_f32 != 0};
-  // box k of an operand into buffer k % 2 (an operand has four or eight); one group
-  // each, empty where there is no operand
+  static_assert(CW % 64 == 0, "an even number of boxes, so that an operand starts at buffer 0");
+  // box k of an operand into buffer k % 2; one group each, empty where there is no operand
   auto request = [&](const EpiOperand& o, int k) {
     if (o.p) epi_fetch(o, stg + (k & 1) * 2048, y0, n0 + (o.f32 ? 16 : 32) * k, M, N);
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -311,10 +311,10 @@ __device__ __forceinline__ void epi_apply(const EpiArgs& e, uint8_t* stg, int y0
     };
     if (!o.f32) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) step(k, 4, [&](const uint8_t* box) { acc.use16(box, k, f); });
+      for (int k = 0; k < CW / 32; ++k) step(k, CW / 32, [&](const uint8_t* box) { acc.use16(box, k, f); });
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) step(k, 8, [&](const uint8_t* box) { acc.use32(box, k, f); });
+      for (int k = 0; k < CW / 16; ++k) step(k, CW / 16, [&](const uint8_t* box) { acc.use32(box, k, f); });
     }
   };
   const EpiOperand nothing{nullptr, 0, 1, false};

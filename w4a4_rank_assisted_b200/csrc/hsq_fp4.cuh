@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
         }
         auto y = [&](int c) { return __uint_as_float(v[c >> 4][c & 15]); };
-        if constexpr (EPI) epi_apply(args.epi, stg, y0, n0, args.M, args.N, EpiRows{v});
+        if constexpr (EPI) epi_apply<128>(args.epi, stg, y0, n0, args.M, args.N, EpiRows{v});
         // store: 32 rows x 128 bytes per TMA box, 128-byte swizzled staging
         if (!args.out_f32) {
 #pragma unroll

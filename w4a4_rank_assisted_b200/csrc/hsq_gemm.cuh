@@ -1354,9 +1354,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       }
       // the accumulators already hold U L2 + b (added by the tile's first unit)
       if constexpr (Cfg::TMA_STORE && Cfg::EPI) {
-        static_assert(CW == 128, "epi_apply");
         if (tc * BN + h * CW < args.N)
-          epi_apply(args.epi, ystage + dw * 4096, tr * TILE_M + static_cast<int>(crank) * BM + q * 32, tc * BN + h * CW,
+          epi_apply<CW>(args.epi, ystage + dw * 4096, tr * TILE_M + static_cast<int>(crank) * BM + q * 32, tc * BN + h * CW,
                     args.M, args.N, EpiQuads<NBLK>{acc2});
       }
       if constexpr (Cfg::TMA_STORE) {

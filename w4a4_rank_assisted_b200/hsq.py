@@ -315,13 +315,19 @@ class Epilogue:
     ``mul``: rows of N values, token m takes row ``m // mul_rows``; ``residual``:
     M rows of N values (Y itself adds onto it in place).  Both may be column
     ranges of wider tensors (last dimension dense, row stride a multiple of 8).
-    The object keeps the tensors and is reused from call to call."""
+    The object keeps the tensors and is reused from call to call; what it was made
+    with is fixed."""
+
+    act = property(lambda self: self._act)
+    mul = property(lambda self: self._mul)
+    mul_rows = property(lambda self: self._mul_rows)
+    residual = property(lambda self: self._residual)
 
     def __init__(self, act: str = "none", mul: Optional[torch.Tensor] = None, mul_rows: int = 1,
                  residual: Optional[torch.Tensor] = None):
         if act not in ACTIVATIONS:
             raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTIVATIONS)})")
-        self.act, self.mul, self.mul_rows, self.residual = act, mul, int(mul_rows), residual
+        self._act, self._mul, self._mul_rows, self._residual = act, mul, int(mul_rows), residual
         c = self._c = _CEpilogue(act=ACTIVATIONS[act], mul_rows=self.mul_rows)
         for name, t in (("mul", mul), ("residual", residual)):
             if t is None:
@@ -336,13 +342,13 @@ class Epilogue:
 
     def _for(self, Y: torch.Tensor, M: int, N: int):
         """The C struct, once the operands' shapes and device are those of Y."""
-        if self.mul is not None and (self.mul_rows < 1 or tuple(self.mul.shape) != (-(-M // self.mul_rows), N)):
-            raise ValueError(f"mul has {tuple(self.mul.shape)} values; {M} tokens at {self.mul_rows} a row, "
-                             f"{N} outputs")
-        if self.residual is not None and tuple(self.residual.shape) != (M, N):
-            raise ValueError(f"residual is {tuple(self.residual.shape)}, Y is {(M, N)}")
-        for t in (self.mul, self.residual):
-            if t is not None and t.device != Y.device:
+        mul, residual = self._mul, self._residual
+        if mul is not None and (self._mul_rows < 1 or tuple(mul.shape) != (-(-M // self._mul_rows), N)):
+            raise ValueError(f"mul has {tuple(mul.shape)} values; {M} tokens at {self._mul_rows} a row, {N} outputs")
+        if residual is not None and tuple(residual.shape) != (M, N):
+            raise ValueError(f"residual is {tuple(residual.shape)}, Y is {(M, N)}")
+        for t in (mul, residual):
+            if t is not None and t.get_device() != Y.get_device():
                 raise ValueError("the epilogue's operands live on another device than Y")
         return ctypes.byref(self._c)
 
@@ -398,7 +404,14 @@ _POS_DTYPES = {torch.int32: HSQ_POS_I32, torch.int64: HSQ_POS_I64, torch.float32
 class Rotation:
     """A rotation of heads by positions (hsq_rotation): ``freqs`` [pairs] fp32,
     ``pair_axes`` the axis of every pair (None: one axis).  The object keeps the
-    frequencies and is reused from call to call."""
+    frequencies and is reused from call to call; what it was made with is fixed."""
+
+    freqs = property(lambda self: self._freqs)
+    pairs = property(lambda self: self._c.pairs)
+    n_axes = property(lambda self: self._n_axes)
+    interleaved = property(lambda self: bool(self._c.interleaved))
+    transpose = property(lambda self: bool(self._c.transpose))
+    scale = property(lambda self: self._c.scale)
 
     def __init__(self, freqs: torch.Tensor, pair_axes=None, interleaved: bool = False, transpose: bool = False,
                  scale: float = 1.0):
@@ -409,11 +422,9 @@ class Rotation:
             raise ValueError(f"{freqs.numel()} frequencies and {len(axes)} pair axes")
         if min(axes) < 0 or max(axes) >= HSQ_ROPE_MAX_AXES:
             raise ValueError(f"axes are 0 .. {HSQ_ROPE_MAX_AXES - 1}")
-        self.freqs, self.pairs, self.n_axes = freqs, len(axes), max(axes) + 1
-        self.interleaved, self.transpose, self.scale = bool(interleaved), bool(transpose), float(scale)
-        self._axes = bytes(axes)
-        self._c = _CRotation(freqs=freqs.data_ptr(), pair_axis=self._axes, pairs=self.pairs, n_axes=self.n_axes,
-                             interleaved=int(self.interleaved), transpose=int(self.transpose), scale=self.scale)
+        self._freqs, self._n_axes, self._axes = freqs, max(axes) + 1, bytes(axes)
+        self._c = _CRotation(freqs=freqs.data_ptr(), pair_axis=self._axes, pairs=len(axes), n_axes=self._n_axes,
+                             interleaved=int(bool(interleaved)), transpose=int(bool(transpose)), scale=float(scale))
         self._ref = ctypes.byref(self._c)
 
 
@@ -444,8 +455,8 @@ def _positions(p: torch.Tensor, rotation: Rotation) -> bytes:
         raise ValueError(f"positions are int32, int64 or float32, not {p.dtype}")
     shape, strides = p.shape, p.stride()
     rows, axes = (shape[0], 1) if len(shape) == 1 else (shape[0], shape[1]) if len(shape) == 2 else (0, 0)
-    if axes != rotation.n_axes or (axes > 1 and strides[1] != 1):
-        raise ValueError(f"positions are [rows, {rotation.n_axes}] with a dense last dimension")
+    if axes != rotation._n_axes or (axes > 1 and strides[1] != 1):
+        raise ValueError(f"positions are [rows, {rotation._n_axes}] with a dense last dimension")
     return _POSITIONS.pack(p.data_ptr(), kind, rows, strides[0] if rows > 1 else axes)
 
 
@@ -475,7 +486,7 @@ def hsq_rope(x: torch.Tensor, y: torch.Tensor, positions: torch.Tensor, rotation
     hy = hx if y is x else _heads(y, "y", shape)
     pos = _positions(positions, rotation)
     index = x.get_device()
-    _same_device(index, y, positions, rotation.freqs)
+    _same_device(index, y, positions, rotation._freqs)
     _check(_on_device(index, stream, lambda s: load().hsq_rope(
         hx, hy, kind, shape[0], shape[1], shape[2], rotation._ref, pos, s)), "hsq_rope")
 
@@ -540,7 +551,7 @@ def hsq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cac
     index = k.get_device()
     if rotation is not None:
         rot = rotation._ref
-        _same_device(index, rotation.freqs)
+        _same_device(index, rotation._freqs)
         if positions is not None:
             pos = _positions(positions, rotation)
     elif positions is not None:
