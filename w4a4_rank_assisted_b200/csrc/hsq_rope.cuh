@@ -12,11 +12,11 @@
 // two heads, pass by pass, the next pass's pieces requested first.  (A thread that
 // formed its own angles and walked over the heads took twice as long.)
 //
-// Bound by memory once there are enough tokens: 20.7 us at 4608 tokens x 48 heads x 128
-// in bf16 (113 MB: 5.5 TB/s, 0.84 of the copy rate), 27 us at 15606 x 16 x 80 in fp32 (160
-// MB: 0.9), 43 us for the append of 9203 tokens of 32 + 8 + 8 heads x 128 (226 MB: 0.8);
-// by launch and latency below: 2.3 us for one token's rotation, 3.2 us for its append
-// (a page lookup is three loads that depend on one another).
+// Bound by memory once there are enough tokens: 20.1 us at 4608 tokens x 48 heads x 128
+// in bf16 (113 MB: 5.6 TB/s, 0.86 of the copy rate), 26.5 us at 15606 x 16 x 80 in fp32
+// (160 MB: 0.92), 43 us for the append of 9203 tokens of 32 + 8 + 8 heads x 128 (226 MB:
+// 0.8); by launch and latency below: 2.3 us for one token's rotation, 3.3 us for its
+// append (a page lookup is loads that depend on one another).
 //
 // The angle: p f_i is formed in fp64 (a product of 24-bit factors is exact there;
 // in fp32, position 10^5 leaves an angle an error of 4e-3), divided by 2 pi, its
@@ -30,8 +30,9 @@ namespace hsq {
 
 constexpr int kRopeMaxPairs = 256;
 constexpr int kRopeThreads = 256;  // most threads of a block
-// Heads of a thread and a pass.  Four hold 16 more registers a piece: at two blocks per
-// SM instead of three 23.5 against 20.7 us (4608 tokens x 48 heads x 128, bf16).
+// Heads of a thread and a pass.  Four leave room for two blocks per SM instead of three:
+// 21.8 against 20.1 us (4608 tokens x 48 heads x 128, bf16), 54 against 26.3 (15606 x 16 x
+// 80, fp32).
 constexpr int kRopeHeads = 2;
 constexpr int kRopeShared = 32768;  // shared memory of a block's tokens: their angles and cache rows
 
@@ -167,9 +168,25 @@ struct RopeUnit {
       pb = ADJ ? b / 2 : a;
     }
   }
+  __device__ __forceinline__ int second() const { return b < 0 ? a : b; }  // (always readable)
   // the pair whose angle is kept at place j (of V)
   __device__ __forceinline__ int pair(int j) const {
     return (ADJ && V > 1) ? (j < V / 2 ? pa + j : pb + j - V / 2) : pa + j;
+  }
+  // cos and sin of the unit's places at one token (ang: its pairs; 16-byte aligned for V > 1)
+  __device__ __forceinline__ void angles(const float2* ang, float (&c)[V], float (&s)[V]) const {
+    if constexpr (V == 1) {
+      const float2 cs = ang[pa];
+      c[0] = cs.x;
+      s[0] = cs.y;
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        const float4 cs = *reinterpret_cast<const float4*>(ang + pair(j));
+        c[j] = cs.x; s[j] = cs.y;
+        c[j + 1] = cs.z; s[j + 1] = cs.w;
+      }
+    }
   }
   // the pieces (p, q) turned by the angles (c, s): x and y of pair j are gathered, two
   // pairs a packed instruction
@@ -212,7 +229,7 @@ struct RopeArgs {
 
 template <typename T, int V, bool ADJ>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 4 : 3) rope_kernel(const __grid_constant__ RopeArgs a) {
-  extern __shared__ float2 rope_angles[];  // [tokens of the block][pairs]
+  extern __shared__ __align__(16) float2 rope_angles[];  // [tokens of the block][pairs]
   grid_dep_wait();  // x comes from the preceding kernel
   if (threadIdx.x == 0) grid_dep_launch();
   const int t = threadIdx.x, P = a.rot.pairs;
@@ -220,20 +237,17 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 4 : 3) rope_ker
   const int t0 = static_cast<int>(blockIdx.x) * a.g.tokens * a.g.passes;  // (below tokens)
   const int n = min(a.g.tokens * a.g.passes, a.tokens - t0);              // tokens of the block
   const int h0 = (static_cast<int>(blockIdx.y) * a.g.splits + sp) * kRopeHeads;
-  // out of range: the block's last token and the last head are read, and nothing is written
-  const T* x = static_cast<const T*>(a.x.data) + static_cast<long long>(t0) * a.x.ts;
-  T* y = static_cast<T*>(a.y.data) + static_cast<long long>(t0) * a.y.ts;
+  // the thread's pieces of its first token; out of range: the block's last token and
+  // the last head are read, and nothing is written
+  RopeUnit<V, ADJ> un(u0, P);
   Piece<T, V> p[kRopeHeads], q[kRopeHeads];
-  auto load = [&](int k, const RopeUnit<V, ADJ>& un) {
-    const T* xk = x + min(k, n - 1) * a.x.ts;
+  const T* x[kRopeHeads];
 #pragma unroll
-    for (int i = 0; i < kRopeHeads; ++i) {
-      const T* xh = xk + min(h0 + i, a.heads - 1) * a.x.hs;
-      p[i].load(xh + un.a);
-      q[i].load(xh + (un.b < 0 ? un.a : un.b));
-    }
-  };
-  load(tk, RopeUnit<V, ADJ>(u0, P));
+  for (int i = 0; i < kRopeHeads; ++i) {
+    x[i] = static_cast<const T*>(a.x.data) + (t0 + min(tk, n - 1)) * a.x.ts + min(h0 + i, a.heads - 1) * a.x.hs;
+    p[i].load(x[i] + un.a);
+    q[i].load(x[i] + un.second());
+  }
   for (int i = t; i < n * P; i += blockDim.x) {
     const int k = i / P, j = i - k * P;
     float c, s;
@@ -242,53 +256,59 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 4 : 3) rope_ker
   }
   __syncthreads();
   if (tk >= a.g.tokens || h0 >= a.heads) return;
-  const int walk = (a.g.units - u0 + a.g.lanes - 1) / a.g.lanes;  // units of this thread
-  for (int k = tk, w = 0; k < n;) {
-    const float2* ang = rope_angles + k * P;
-    T* yk = y + k * a.y.ts;
-    const RopeUnit<V, ADJ> un(u0 + w * a.g.lanes, P);
+  T* y = static_cast<T*>(a.y.data) + (t0 + tk) * a.y.ts + h0 * a.y.hs;
+  const long long x_step = a.g.tokens * a.x.ts, y_step = a.g.tokens * a.y.ts;
+  int u = u0;
+  for (int k = tk; k < n;) {
+    const RopeUnit<V, ADJ> now = un;
+    T* yk = y;
+    float c[V], s[V];
+    if (now.b >= 0) now.angles(rope_angles + k * P, c, s);
     Piece<T, V> pc[kRopeHeads], qc[kRopeHeads];
 #pragma unroll
     for (int i = 0; i < kRopeHeads; ++i) {
       pc[i] = p[i];
       qc[i] = q[i];
     }
-    if (++w == walk) {
-      w = 0;
+    // the next pass's pieces (with V > 1 a thread has one unit of every token)
+    if (V == 1 && (u += a.g.lanes) < a.g.units) {
+      un = RopeUnit<V, ADJ>(u, P);
+    } else {
       k += a.g.tokens;
-    }
-    if (k < n) load(k, RopeUnit<V, ADJ>(u0 + w * a.g.lanes, P));  // the next pass's pieces
-    float c[V], s[V];
-    if (un.b >= 0) {
+      y += y_step;
+      if constexpr (V == 1) un = RopeUnit<V, ADJ>(u = u0, P);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 cs = ang[un.pair(j)];
-        c[j] = cs.x;
-        s[j] = cs.y;
+      for (int i = 0; i < kRopeHeads; ++i) x[i] += x_step;
+    }
+    if (k < n) {
+#pragma unroll
+      for (int i = 0; i < kRopeHeads; ++i) {
+        p[i].load(x[i] + un.a);
+        q[i].load(x[i] + un.second());
       }
     }
 #pragma unroll
     for (int i = 0; i < kRopeHeads; ++i) {
       if (h0 + i >= a.heads) break;
-      T* yh = yk + (h0 + i) * a.y.hs;
       float f[V], g[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         f[j] = pc[i].at(j);
         g[j] = qc[i].at(j);
       }
-      if (un.b >= 0) {
+      if (now.b >= 0) {
         RopeUnit<V, ADJ>::rotate(f, g, c, s);
-        store_piece<V>(yh + un.b, g);
+        store_piece<V>(yk + now.b, g);
       }
-      store_piece<V>(yh + un.a, f);
+      store_piece<V>(yk + now.a, f);
+      yk += a.y.hs;
     }
   }
 }
 
 struct CacheView {
   void* data;
-  long long ps, ss, hs;  // elements between pages, between slots, between heads
+  long long ps, ss, hs;  // elements between pages, between slots, between heads (k's and v's alike)
   const float* scale;    // E4M3: [kv_heads], or nullptr for 1
 };
 
@@ -339,7 +359,7 @@ struct AppendToken {
 // C: the cache's element type.
 template <typename T, typename C, int V, bool ADJ>
 __global__ void __launch_bounds__(kRopeThreads, 3) kv_append_kernel(const __grid_constant__ AppendArgs a) {
-  extern __shared__ float2 rope_angles[];  // [tokens of the block][pairs], then the tokens
+  extern __shared__ __align__(16) float2 rope_angles[];  // [tokens of the block][pairs], then the tokens
   AppendToken* toks = reinterpret_cast<AppendToken*>(rope_angles + a.g.tokens * a.g.passes * a.rot.pairs);
   grid_dep_wait();
   if (threadIdx.x == 0) grid_dep_launch();
@@ -408,14 +428,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) kv_append_kernel(const __grid
     if (k < n) load(k, RopeUnit<V, ADJ>(u0 + w * a.g.lanes, P));  // the next pass's pieces
     if (me.pos < 0) continue;
     float c[V], s[V];
-    if (un.b >= 0) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float2 cs = ang[un.pair(j)];
-        c[j] = cs.x;
-        s[j] = cs.y;
-      }
-    }
+    if (un.b >= 0) un.angles(ang, c, s);
 #pragma unroll
     for (int i = 0; i < kRopeHeads; ++i) {
       const int e = h0 + i;
