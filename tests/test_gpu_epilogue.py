@@ -220,6 +220,11 @@ def test_epilogue_refusals_of_the_binding():
                dict(residual=z(16, 72)), dict(residual=z(1, 64))):
         with pytest.raises(ValueError):
             lay("x", Y, hsq.Epilogue(**kw))
+    for bad in (z(15, 64), z(16, 72), z(16, 64, dt=torch.float32), z(16, 64, dt=torch.float16)):  # not what is written
+        with pytest.raises(ValueError):
+            hsq.hsq_linear_forward_x_ep(lay.X, lay.pl.s, lay.pl.L1, lay.pl.w_codes, lay.pl.w_scales, None, lay.pl.L2,
+                                        lay.pl.bias, 16, 64, 64, 4, bad, hsq.Epilogue("relu"),
+                                        workspace=lay.pl.workspace_x(16), ws_bytes=lay.pl.workspace_x(16).numel())
     for kw in (dict(mul=z(64, 16).t()), dict(residual=z(16, 64, dt=torch.float16)), dict(residual=z(64))):
         with pytest.raises(ValueError):
             hsq.Epilogue(**kw)

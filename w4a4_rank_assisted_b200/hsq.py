@@ -353,7 +353,12 @@ class Epilogue:
         return ctypes.byref(self._c)
 
 
-def _ep(epilogue: Optional[Epilogue], Y, M, N):
+def _ep(epilogue: Optional[Epilogue], Y, M, N, out, *inputs):
+    """The epilogue's C struct (None for none), once Y has the shape and type that the
+    call writes and the call's tensors live on one device."""
+    if tuple(Y.shape) != (M, N) or _out_dtype(Y, "Y") != out:
+        raise ValueError(f"Y is {tuple(Y.shape)} {Y.dtype}, the call writes {(M, N)} with out={out}")
+    _same_device(Y.get_device(), *inputs)
     return None if epilogue is None else epilogue._for(Y, M, N)
 
 
@@ -361,38 +366,38 @@ def hsq_linear_forward_ep(x_codes, x_scales, U, w_codes, w_scales, w_e4m3, L2, b
                           epilogue: Optional[Epilogue], out: int = HSQ_OUT_BF16, workspace=None, ws_bytes: int = 0,
                           group=GROUP, stream=None) -> None:
     """hsq_linear_forward (w_e4m3 None) or hsq_linear_forward_pre with an epilogue."""
-    _check(load().hsq_linear_forward_ep(_ptr(x_codes), _ptr(x_scales), _ptr(U), _ptr(w_codes), _ptr(w_scales),
-                                        _ptr(w_e4m3), _ptr(L2), _ptr(bias), M, N, K, r, group, _ptr(Y), int(out),
-                                        _ep(epilogue, Y, M, N), _ptr(workspace), int(ws_bytes), _stream(stream)),
-           "hsq_linear_forward_ep")
+    ep = _ep(epilogue, Y, M, N, out, x_codes, w_codes, w_e4m3, workspace)
+    _check(_on_device(Y.get_device(), stream, lambda s: load().hsq_linear_forward_ep(
+        _ptr(x_codes), _ptr(x_scales), _ptr(U), _ptr(w_codes), _ptr(w_scales), _ptr(w_e4m3), _ptr(L2), _ptr(bias), M, N,
+        K, r, group, _ptr(Y), int(out), ep, _ptr(workspace), int(ws_bytes), s)), "hsq_linear_forward_ep")
 
 
 def hsq_linear_forward_x_ep(X, s, L1, w_codes, w_scales, w_e4m3, L2, bias, M, N, K, r, Y,
                             epilogue: Optional[Epilogue], out: int = HSQ_OUT_BF16, workspace=None, ws_bytes: int = 0,
                             group=GROUP, stream=None) -> None:
     """hsq_linear_forward_x with an epilogue."""
-    _check(load().hsq_linear_forward_x_ep(_ptr(X), _ptr(s), _ptr(L1), _ptr(w_codes), _ptr(w_scales), _ptr(w_e4m3),
-                                          _ptr(L2), _ptr(bias), M, N, K, r, group, _ptr(Y), int(out),
-                                          _ep(epilogue, Y, M, N), _ptr(workspace), int(ws_bytes), _stream(stream)),
-           "hsq_linear_forward_x_ep")
+    ep = _ep(epilogue, Y, M, N, out, X, w_codes, w_e4m3, workspace)
+    _check(_on_device(Y.get_device(), stream, lambda st: load().hsq_linear_forward_x_ep(
+        _ptr(X), _ptr(s), _ptr(L1), _ptr(w_codes), _ptr(w_scales), _ptr(w_e4m3), _ptr(L2), _ptr(bias), M, N, K, r, group,
+        _ptr(Y), int(out), ep, _ptr(workspace), int(ws_bytes), st)), "hsq_linear_forward_x_ep")
 
 
 def hsq_linear_forward_fused_ep(X, s, L1, w_codes, w_scales, L2, bias, M, N, K, r, Y, epilogue: Optional[Epilogue],
                                 out: int = HSQ_OUT_BF16, group=GROUP, stream=None) -> None:
     """hsq_linear_forward_fused with an epilogue."""
-    _check(load().hsq_linear_forward_fused_ep(_ptr(X), _ptr(s), _ptr(L1), _ptr(w_codes), _ptr(w_scales), _ptr(L2),
-                                              _ptr(bias), M, N, K, r, group, _ptr(Y), int(out),
-                                              _ep(epilogue, Y, M, N), _stream(stream)),
-           "hsq_linear_forward_fused_ep")
+    ep = _ep(epilogue, Y, M, N, out, X, w_codes)
+    _check(_on_device(Y.get_device(), stream, lambda st: load().hsq_linear_forward_fused_ep(
+        _ptr(X), _ptr(s), _ptr(L1), _ptr(w_codes), _ptr(w_scales), _ptr(L2), _ptr(bias), M, N, K, r, group, _ptr(Y),
+        int(out), ep, st)), "hsq_linear_forward_fused_ep")
 
 
 def hsq_fp4_linear_forward_ep(x_codes, x_sf, x_gs, U, w_codes, w_sf, w_gs, L2, bias, M, N, K, r, Y,
                               epilogue: Optional[Epilogue], out: int = HSQ_OUT_BF16, stream=None) -> None:
     """hsq_fp4_linear_forward with an epilogue."""
-    _check(load().hsq_fp4_linear_forward_ep(_ptr(x_codes), _ptr(x_sf), _ptr(x_gs), _ptr(U), _ptr(w_codes),
-                                            _ptr(w_sf), _ptr(w_gs), _ptr(L2), _ptr(bias), M, N, K, r, _ptr(Y),
-                                            int(out), _ep(epilogue, Y, M, N), _stream(stream)),
-           "hsq_fp4_linear_forward_ep")
+    ep = _ep(epilogue, Y, M, N, out, x_codes, w_codes)
+    _check(_on_device(Y.get_device(), stream, lambda s: load().hsq_fp4_linear_forward_ep(
+        _ptr(x_codes), _ptr(x_sf), _ptr(x_gs), _ptr(U), _ptr(w_codes), _ptr(w_sf), _ptr(w_gs), _ptr(L2), _ptr(bias), M,
+        N, K, r, _ptr(Y), int(out), ep, s)), "hsq_fp4_linear_forward_ep")
 
 
 # ---------------------------------------------------------------- rotary positions, cache append
