@@ -117,6 +117,7 @@ SHAPES = [
     ("codes", "nvfp4", 1, 192, 264, 4, 64),
     ("codes", "nvfp4", 130, 320, 392, 0, 64),
     ("codes", "nvfp4", 1000, 512, 2056, 32, 64),
+    ("x", "int4", 520, 640, 392, 32, 64),        # large tiles, many ranks
 ]
 ACTS = ["silu", "gelu_tanh", "gelu_erf", "relu", "none"]
 

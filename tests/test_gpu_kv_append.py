@@ -261,6 +261,27 @@ def test_graph_replay_with_changed_lengths():
     torch.cuda.synchronize()
 
 
+def test_two_appends_at_once():
+    """Two batches into caches of their own, on two streams: each as alone."""
+    f = ladder(64)
+    rot = hsq.Rotation(f)
+    b = [Batch([200, 40, 7], [3, 60, 0], 16, 4, 8, 128, BF, BF, seed=s, cu=True) for s in (1, 2)]
+    alone = []
+    for x in b:
+        kc, vc, q = x.kc.clone(), x.vc.clone(), x.q_out.clone()
+        hsq.hsq_kv_append(x.k, x.v, kc, vc, x.table, x.lens_t, cu_seqlens=x.cu, rotation=rot, q=x.q, q_out=q)
+        alone.append((kc, vc, q))
+    streams = [torch.cuda.Stream() for _ in b]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, st in zip(b, streams):
+            hsq.hsq_kv_append(x.k, x.v, x.kc, x.vc, x.table, x.lens_t, cu_seqlens=x.cu, rotation=rot, q=x.q, q_out=x.q_out,
+                              stream=st)
+    torch.cuda.synchronize()
+    for x, want in zip(b, alone):
+        assert all(torch.equal(g, w) for g, w in zip((x.kc, x.vc, x.q_out), want))
+
+
 def test_long_cache_offsets_pass_32_bits():
     """A cache of more than 2^31 elements: its last pages are reached (bf16, 4.6 GB each of k and v)."""
     page, kv, D = 64, 8, 128

@@ -192,8 +192,7 @@ __device__ __forceinline__ float2 epi_pair16(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// How the threads hold the warp's accumulators of 32 rows, and read a
-// box for them: use16 / use32 apply f(z, operand) to the pairs of neighbouring
+// How the threads hold the warp's accumulators of 32 rows, and read a box for them: use16 / use32 apply f(z, operand) to the pairs of neighbouring
 // columns in a box of 32 bf16 / 16 fp32 columns, the k-th of the warp's.
 //   Quads: tcgen05.ld 16x256b: lane l has rows l / 4 + 8i and columns 8b + 2 (l % 4), + 1
 template <int NBLK>
@@ -322,9 +321,11 @@ __device__ __forceinline__ void epi_apply(const EpiArgs& e, uint8_t* stg, int y0
   if (res.p) boxes(res, nothing, [](float2& z, const float2& r) { z = __fadd2_rn(z, r); });
 }
 
-// act(z) * mul + residual in place on accumulators of R output features feature(i) by 2 B tokens token(t),
-// the pair z(i, b) holding tokens 2b and 2b + 1 of the thread: operands by elements, a
-// batch requested at a time.
+// act(z) * mul + residual in place on accumulators of R output features feature(i) by
+// 2 B tokens token(t) (the decode tiles), the pair z(i, b) holding tokens 2b and 2b + 1
+// of the thread: operands by elements, a batch of up to 32 requested at a time (one
+// feature at a time, with the activation chosen inside, 30.2 instead of 26.2 us at M =
+// 16, K = 12288, N = 4096; 25.6 without an epilogue).
 template <int R, int B, class T, class Z, class Feature, class Token, class F>
 __device__ __forceinline__ void epi_columns_operand(const T* p, long long ld, int rows, Z&& z, Feature&& feature,
                                                     Token&& token, F&& f) {

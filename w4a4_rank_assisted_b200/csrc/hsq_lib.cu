@@ -837,7 +837,8 @@ uintptr_t view_bits(const hsq_heads& v, int tokens, int heads, size_t es) {
 
 // The widest piece (elements) that a head's layout allows: 16 bytes of input, for
 // bf16 also 8 bytes, else single elements.  `bits`: view_bits of every tensor,
-// scaled to the input's element size.
+// scaled to the input's element size.  Measured at 4608 tokens x 48 heads x 128: 16 / 8
+// bytes / an element 20 - 22 / 26 / 44 us in bf16, 37 / - / 53 in fp32.
 int piece_width(hsq_dtype t, int dim, int pairs, uintptr_t bits) {
   const int es = static_cast<int>(dtype_bytes(t));
   for (int v : {16 / es, 4}) {
