@@ -274,6 +274,24 @@ def test_captured_and_replayed_on_another_stream(form, M):
     torch.cuda.synchronize()
 
 
+def test_offsets_pass_32_bits():
+    """Y, mul and residual of more than 2^31 elements: the last rows equal a call on them alone (the same kernels: both
+    are many tokens)."""
+    M, K, N = 262144, 64, 8320
+    lay = Layer(5000, K, N, 4, seed=1)
+    X = torch.randn(M, K, device=DEV).to(torch.bfloat16)
+    mul = torch.empty(M, N, device=DEV, dtype=torch.bfloat16)
+    mul[-5000:] = torch.randn(5000, N, device=DEV)
+    Y = torch.empty(M, N, device=DEV, dtype=torch.bfloat16)
+    Y[-5000:] = torch.randn(5000, N, device=DEV)
+    want, old = torch.empty(5000, N, device=DEV, dtype=torch.bfloat16), Y[-5000:].clone()
+    hsq.forward_x(lay.pl, X, Y, lay.pl.workspace_x(M), epilogue=hsq.Epilogue("silu", mul=mul, residual=Y))
+    hsq.forward_x(lay.pl, X[-5000:].clone(), want, lay.pl.workspace_x(5000),
+                  epilogue=hsq.Epilogue("silu", mul=mul[-5000:], residual=old))
+    assert torch.equal(Y[-5000:], want)
+    assert hsq.hsq_get_device_status() == hsq.HSQ_OK
+
+
 def test_epilogue_against_the_oracle():
     """The whole layer from the oracle's z in fp64: the spec's tolerance through the activation (|act'| <= 1.13)."""
     M, K, N, r = 37, 448, 264, 4

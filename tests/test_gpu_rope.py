@@ -184,6 +184,22 @@ def test_non_finite_values_stay_in_their_pair():
     assert torch.equal(bad, want) and y[1, 1, 40] == float("inf")
 
 
+def test_offsets_pass_32_bits():
+    """More than 2^31 elements of x and y: the last tokens equal a call on them alone."""
+    T, H, D = 70000, 64, 512
+    freqs = _plain()[1]
+    x = torch.empty(T, H, D, device=DEV, dtype=torch.bfloat16)
+    x[-3:] = torch.randn(3, H, D, device=DEV)
+    x[:2] = torch.randn(2, H, D, device=DEV)
+    pos = torch.arange(T, device=DEV)
+    y, rot = torch.empty_like(x), hsq.Rotation(freqs, interleaved=True)
+    hsq.hsq_rope(x, y, pos, rot)
+    for part in (slice(0, 2), slice(T - 3, T)):
+        want = torch.empty_like(x[part])
+        hsq.hsq_rope(x[part], want, pos[part], rot)
+        assert torch.equal(y[part], want)
+
+
 def test_refusals_of_the_binding():
     x, freqs = _plain()
     rot, pos, y = hsq.Rotation(freqs), torch.arange(5, device=DEV), torch.empty_like(x)
