@@ -301,11 +301,12 @@ hsq_status hsq_linear_forward_fused(const void* X_bf16, const float* s, const vo
  * is the forward without it, bit for bit.
  * The paper has no counterpart: in a transformer block these steps follow the
  * linear's output elementwise.
- *   hsq_linear_forward_ep        hsq_linear_forward, or hsq_linear_forward_pre
- *                                where w_e4m3 is not NULL (workspace as for those)
- *   hsq_linear_forward_x_ep      hsq_linear_forward_x
- *   hsq_linear_forward_fused_ep  hsq_linear_forward_fused
- *   hsq_fp4_linear_forward_ep    hsq_fp4_linear_forward (below)
+ *   hsq_linear_forward_ep          hsq_linear_forward, or hsq_linear_forward_pre
+ *                                  where w_e4m3 is not NULL (workspace as for those)
+ *   hsq_linear_forward_noalloc_ep  hsq_linear_forward_noalloc
+ *   hsq_linear_forward_x_ep        hsq_linear_forward_x
+ *   hsq_linear_forward_fused_ep    hsq_linear_forward_fused
+ *   hsq_fp4_linear_forward_ep      hsq_fp4_linear_forward (below)
  */
 typedef enum {
   HSQ_ACT_NONE = 0,
@@ -332,6 +333,12 @@ hsq_status hsq_linear_forward_ep(const uint8_t* x_codes, const float* x_scales, 
                                  int M, int N, int K, int r, int group,
                                  void* Y, hsq_out_dtype out, const hsq_epilogue* ep,
                                  void* workspace, size_t ws_bytes, cudaStream_t stream);
+hsq_status hsq_linear_forward_noalloc_ep(const uint8_t* x_codes, const float* x_scales, const float* U,
+                                         const uint8_t* w_codes, const float* w_scales,
+                                         const void* L2_bf16, const void* bias_bf16,
+                                         int M, int N, int K, int r, int group,
+                                         void* Y, hsq_out_dtype out, const hsq_epilogue* ep,
+                                         cudaStream_t stream);
 hsq_status hsq_linear_forward_x_ep(const void* X_bf16, const float* s, const void* L1_bf16,
                                    const uint8_t* w_codes, const float* w_scales, const uint8_t* w_e4m3,
                                    const void* L2_bf16, const void* bias_bf16,

@@ -23,12 +23,14 @@ def _epilogue(**kw):
 
 
 def _forwards():
-    """The four calls with an epilogue on a 16 x 64 Y at address A (K = 64, r = 4)."""
+    """The calls with an epilogue on a 16 x 64 Y at address A (K = 64, r = 4)."""
     lib = hsq.load()
     far = 1 << 30
     return {
         "codes": lambda e: lib.hsq_linear_forward_ep(far, far, far, far, far, None, far, None, 16, 64, 64, 4, 64, A, 0, e,
                                                      far, 0, None),
+        "noalloc": lambda e: lib.hsq_linear_forward_noalloc_ep(far, far, far, far, far, far, None, 16, 64, 64, 4, 64, A, 0,
+                                                               e, None),
         "x": lambda e: lib.hsq_linear_forward_x_ep(far, far, far, far, far, None, far, None, 16, 64, 64, 4, 64, A, 0, e,
                                                    far, 0, None),
         "fused": lambda e: lib.hsq_linear_forward_fused_ep(far, far, far, far, far, far, None, 16, 64, 64, 4, 64, A, 0, e,
@@ -38,7 +40,7 @@ def _forwards():
     }
 
 
-@pytest.mark.parametrize("form", ["codes", "x", "fused", "fp4"])
+@pytest.mark.parametrize("form", ["codes", "noalloc", "x", "fused", "fp4"])
 def test_epilogue_refusals(form):
     f = _forwards()[form]
     assert f(_epilogue(act=5)) == INVALID

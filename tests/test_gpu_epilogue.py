@@ -178,6 +178,24 @@ def test_in_place_residual_and_mul(i):
         assert torch.equal(Y, want)
 
 
+@pytest.mark.parametrize("M,K,group", [(3, 512, 64), (12, 2048, 64), (100, 640, 64), (300, 512, 128)])
+def test_forward_without_allocation(M, K, group):
+    """hsq_linear_forward_noalloc_ep, twice in a row: the bits of the call with a workspace."""
+    lay = Layer(M, K, 392, 4, group, seed=M)
+    pl, s = lay.pl, lay.spec
+    res = torch.randn(M, 392, device=DEV).to(torch.bfloat16)
+    ep = hsq.Epilogue("gelu_tanh", residual=res)
+    want = torch.empty(M, 392, device=DEV, dtype=torch.bfloat16)
+    lay("codes", want, ep)
+    act = hsq.ActBuffers(M, K, 4, DEV, group)
+    hsq.hsq_quantize_act(lay.X, pl.s, pl.L1, M, K, 4, act.x_codes, act.x_scales, act.U, group=group)
+    for _ in range(2):
+        Y = torch.empty_like(want)
+        hsq.hsq_linear_forward_noalloc_ep(act.x_codes, act.x_scales, act.U, pl.w_codes, pl.w_scales, pl.L2, pl.bias, M,
+                                          s.N, K, 4, Y, ep, group=group)
+        assert torch.equal(Y, want)
+
+
 @pytest.mark.parametrize("form,M", [("fused", 2), ("codes", 12), ("x", 150), ("x", 600)])
 def test_large_values_and_non_finite_operands(form, M):
     """z far outside the exponential's range (through the bias), and infinities and NaN in mul and residual."""

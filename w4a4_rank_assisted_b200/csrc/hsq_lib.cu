@@ -1589,6 +1589,14 @@ hsq_status hsq_linear_forward_noalloc(const uint8_t* x_codes, const float* x_sca
                                       const uint8_t* w_codes, const float* w_scales, const void* L2_bf16,
                                       const void* bias_bf16, int M, int N, int K, int r, int group, void* Y,
                                       hsq_out_dtype out, cudaStream_t stream) {
+  return hsq_linear_forward_noalloc_ep(x_codes, x_scales, U, w_codes, w_scales, L2_bf16, bias_bf16, M, N, K, r, group,
+                                       Y, out, nullptr, stream);
+}
+
+hsq_status hsq_linear_forward_noalloc_ep(const uint8_t* x_codes, const float* x_scales, const float* U,
+                                         const uint8_t* w_codes, const float* w_scales, const void* L2_bf16,
+                                         const void* bias_bf16, int M, int N, int K, int r, int group, void* Y,
+                                         hsq_out_dtype out, const hsq_epilogue* ep, cudaStream_t stream) {
   // The same argument checks as hsq_linear_forward, made before the scratch is touched,
   // so that a rejected call launches nothing.
   hsq_status st = check_common(M, K, r, group);
@@ -1602,6 +1610,8 @@ hsq_status hsq_linear_forward_noalloc(const uint8_t* x_codes, const float* x_sca
       !aligned16(Y) || (U && !aligned16(U)) || (L2_bf16 && !aligned16(L2_bf16)) ||
       (bias_bf16 && !aligned16(bias_bf16)))
     return HSQ_ERR_ALIGNMENT;
+  st = check_epilogue(&ep, M, N, Y, out);
+  if (st != HSQ_OK) return st;
   const Plan p = make_plan(M, N, K, group, device_sm_count());
   void* scratch = nullptr;
   if (p.ws_bytes() > 0) {
@@ -1611,8 +1621,8 @@ hsq_status hsq_linear_forward_noalloc(const uint8_t* x_codes, const float* x_sca
     // the split-K counters must start at zero; the partial tiles are written before they are read
     if (cudaMemsetAsync(scratch, 0, p.counters_bytes, stream) != cudaSuccess) return HSQ_ERR_CUDA;
   }
-  return hsq_linear_forward(x_codes, x_scales, U, w_codes, w_scales, L2_bf16, bias_bf16, M, N, K, r, group, Y, out,
-                            scratch, scratch ? kNoallocScratchBytes : 0, stream);
+  return forward_impl(x_codes, x_scales, U, w_codes, w_scales, nullptr, L2_bf16, bias_bf16, M, N, K, r, group, Y, out,
+                      ep, scratch, scratch ? kNoallocScratchBytes : 0, stream);
 }
 
 hsq_status hsq_linear_forward_fused(const void* X_bf16, const float* s, const void* L1_bf16, const uint8_t* w_codes,

@@ -48,7 +48,7 @@ EXPORTED = (
     "hsq_lowrank_workspace_bytes", "hsq_lowrank_init",
     "hsq_fp4_codes_bytes", "hsq_fp4_scales_bytes", "hsq_fp4_pack_weights", "hsq_fp4_quantize_act",
     "hsq_fp4_linear_forward",
-    "hsq_linear_forward_ep", "hsq_linear_forward_x_ep", "hsq_linear_forward_fused_ep", "hsq_fp4_linear_forward_ep",
+    "hsq_linear_forward_ep", "hsq_linear_forward_noalloc_ep", "hsq_linear_forward_x_ep", "hsq_linear_forward_fused_ep", "hsq_fp4_linear_forward_ep",
     "hsq_rope", "hsq_kv_append",
 )
 
@@ -155,6 +155,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.hsq_fp4_linear_forward.restype = i
     lib.hsq_linear_forward_ep.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, i, vp, vp, sz, vp]
     lib.hsq_linear_forward_ep.restype = i
+    lib.hsq_linear_forward_noalloc_ep.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, i, vp, vp]
+    lib.hsq_linear_forward_noalloc_ep.restype = i
     lib.hsq_linear_forward_x_ep.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, i, vp, vp, sz, vp]
     lib.hsq_linear_forward_x_ep.restype = i
     lib.hsq_linear_forward_fused_ep.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, i, vp, vp]
@@ -370,6 +372,16 @@ def hsq_linear_forward_ep(x_codes, x_scales, U, w_codes, w_scales, w_e4m3, L2, b
     _check(_on_device(Y.get_device(), stream, lambda s: load().hsq_linear_forward_ep(
         _ptr(x_codes), _ptr(x_scales), _ptr(U), _ptr(w_codes), _ptr(w_scales), _ptr(w_e4m3), _ptr(L2), _ptr(bias), M, N,
         K, r, group, _ptr(Y), int(out), ep, _ptr(workspace), int(ws_bytes), s)), "hsq_linear_forward_ep")
+
+
+def hsq_linear_forward_noalloc_ep(x_codes, x_scales, U, w_codes, w_scales, L2, bias, M, N, K, r, Y,
+                                  epilogue: Optional[Epilogue], out: int = HSQ_OUT_BF16, group=GROUP,
+                                  stream=None) -> None:
+    """hsq_linear_forward_noalloc with an epilogue."""
+    ep = _ep(epilogue, Y, M, N, out, x_codes, w_codes)
+    _check(_on_device(Y.get_device(), stream, lambda s: load().hsq_linear_forward_noalloc_ep(
+        _ptr(x_codes), _ptr(x_scales), _ptr(U), _ptr(w_codes), _ptr(w_scales), _ptr(L2), _ptr(bias), M, N, K, r, group,
+        _ptr(Y), int(out), ep, s)), "hsq_linear_forward_noalloc_ep")
 
 
 def hsq_linear_forward_x_ep(X, s, L1, w_codes, w_scales, w_e4m3, L2, bias, M, N, K, r, Y,
