@@ -19,6 +19,8 @@
 // z, where 1 + erf cancels, at two special-function instructions like the others.
 #pragma once
 
+#include <type_traits>
+
 #include "hsq_device.cuh"
 
 namespace hsq {
@@ -32,6 +34,16 @@ struct EpiArgs {
   long long mul_ld, res_ld;
   int act, mul_rows, mul_f32, res_f32;
 };
+
+// A kernel's arguments: those of its plain form, and an epilogue's behind them in the
+// instantiations that apply one.  (With one structure for both, the plain NVFP4 GEMM
+// was compiled differently and took 1.1 % longer at each of FLUX.1's layers.)
+template <class Args>
+struct WithEpilogue : Args {
+  EpiArgs epi;
+};
+template <class Args, bool EPI>
+using KernelArgs = std::conditional_t<EPI, WithEpilogue<Args>, Args>;
 
 // z / (1 + 2^t) of two values: two special-function instructions each.  2^t overflows
 // to infinity, whose reciprocal is 0, where the quotient is below 2^-126 |z|.

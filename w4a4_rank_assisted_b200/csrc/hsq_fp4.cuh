@@ -40,7 +40,6 @@ struct Fp4Args {
   int tiles_m, tiles_n;
   int out_f32;
   uint64_t limit_ns;
-  EpiArgs epi;  // kernels with EPI: act, mul and residual (hsq_epilogue.cuh)
 };
 
 // Tile 128 tokens x BN outputs; a stage is K = 256 (KCS = 4 chunks of K = 64).
@@ -87,7 +86,7 @@ struct Fp4Cfg {
 template <class Cfg, bool EPI = false>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                    const __grid_constant__ CUtensorMap tm_y, const Fp4Args args) {
+                    const __grid_constant__ CUtensorMap tm_y, const KernelArgs<Fp4Args, EPI> args) {
   constexpr int BM = Cfg::BM, BN = Cfg::BN, STAGES = Cfg::STAGES, KCS = Cfg::KCS, NTM = Cfg::NTM;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

@@ -126,7 +126,6 @@ struct GemmArgs {
   float* fx_U;
   unsigned* fx_bar;
   int fx_zero_words;
-  EpiArgs epi;  // kernels with EPI: act, mul and residual (hsq_epilogue.cuh)
 };
 
 template <int BN_, int DH_, int STAGES_, bool SWAP_, int GPS_, int NI8_, int NTM_, int UNPACK_WARPS_ = 6,
@@ -657,7 +656,7 @@ __device__ __forceinline__ bool grid_barrier(unsigned* bar, uint64_t limit_ns, v
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     w4a4_gemm_kernel(const __grid_constant__ CUtensorMap tm_row, const __grid_constant__ CUtensorMap tm_col,
-                     const __grid_constant__ CUtensorMap tm_y, const GemmArgs args) {
+                     const __grid_constant__ CUtensorMap tm_y, const KernelArgs<GemmArgs, Cfg::EPI> args) {
   constexpr int BM = Cfg::BM, BN = Cfg::BN, CW = Cfg::CW, STAGES = Cfg::STAGES, GPS = Cfg::GPS;
   constexpr int NI8 = Cfg::NI8E, NTM = Cfg::NTM;
   constexpr bool PAIR = Cfg::PAIR;

@@ -52,7 +52,6 @@ struct GemvArgs {
   const float* s;           // [K]
   const __nv_bfloat16* L1;  // [K][r]
   int K, group;
-  EpiArgs epi;  // kernels with EPI: act, mul and residual (hsq_epilogue.cuh)
 };
 
 // Block: warp 0 streams the weights (one elected lane issues bulk copies),
@@ -136,7 +135,7 @@ __device__ __forceinline__ void gemv_compute_sync() { named_bar_sync(1, kGemvCom
 // EPI: with act, mul and residual.
 template <int MT, int LPG, int RF = -1, bool EPI = false>
 __global__ void __launch_bounds__(kGemvThreads, 1)
-    w4a4_gemv_kernel(const __grid_constant__ CUtensorMap tm_sw, const GemvArgs a) {
+    w4a4_gemv_kernel(const __grid_constant__ CUtensorMap tm_sw, const KernelArgs<GemvArgs, EPI> a) {
   extern __shared__ __align__(16) uint8_t gemv_smem[];
   const int W4 = a.Kp / 8;  // packed 32-bit words per row
   const int rowbytes = a.Kp / 2;

@@ -563,7 +563,8 @@ hsq::EpiArgs epi_args(const hsq_epilogue& e) {
 
 template <class Cfg>
 hsq_status launch_gemm(const Plan& p, const CUtensorMap& tr, const CUtensorMap& tc, const CUtensorMap& ty,
-                       const hsq::GemmArgs& a, cudaStream_t st) {
+                       const hsq::WithEpilogue<hsq::GemmArgs>& args, cudaStream_t st) {
+  const hsq::KernelArgs<hsq::GemmArgs, Cfg::EPI>& a = args;
   static std::mutex mu;
   static bool attr_set[64] = {false};
   int dev = 0;
@@ -616,8 +617,9 @@ hsq_status launch_gemm(const Plan& p, const CUtensorMap& tr, const CUtensorMap& 
 // barrier, so every CTA must be resident at once -- a cooperative launch, after
 // the occupancy check.
 template <class Cfg>
-hsq_status launch_gemm_fused(const Plan& p, const CUtensorMap& tr, const CUtensorMap& tc, const hsq::GemmArgs& a,
-                             cudaStream_t st) {
+hsq_status launch_gemm_fused(const Plan& p, const CUtensorMap& tr, const CUtensorMap& tc,
+                             const hsq::WithEpilogue<hsq::GemmArgs>& args, cudaStream_t st) {
+  const hsq::KernelArgs<hsq::GemmArgs, Cfg::EPI>& a = args;
   static_assert(Cfg::FUSED && !Cfg::REALLOC, "fused decode tiles");
   static std::mutex mu;
   static int max_blocks[64] = {0};  // resident CTAs per SM, per device (0: not asked yet)
@@ -673,7 +675,8 @@ hsq_status launch_gemm_fused(const Plan& p, const CUtensorMap& tr, const CUtenso
 // `a` has the shape, rows_per_block and pointers set; the ring layout and the
 // wait limit are filled in here.
 template <int MT, int LPG, int RF = -1, bool EPI = false>
-hsq_status launch_gemv(const Plan& p, hsq::GemvArgs a, cudaStream_t st) {
+hsq_status launch_gemv(const Plan& p, const hsq::WithEpilogue<hsq::GemvArgs>& args, cudaStream_t st) {
+  hsq::KernelArgs<hsq::GemvArgs, EPI> a = args;
   static std::mutex mu;
   static bool attr_set[64] = {false};
   int dev = 0;
@@ -988,7 +991,7 @@ hsq_status forward_fused_dec16(const void* X_bf16, const float* s, const void* L
   if (st != HSQ_OK) return st;
   uint8_t* base = static_cast<uint8_t*>(scr);
 
-  hsq::GemmArgs a{};
+  hsq::WithEpilogue<hsq::GemmArgs> a{};
   CUtensorMap tm_row, tm_col;
   a.scales_r = w_scales; a.ld_r = ldw; a.rows_r = N;
   a.scales_c = reinterpret_cast<float*>(base + o_sc); a.ld_c = ldx; a.rows_c = M;
@@ -1315,7 +1318,7 @@ static hsq_status forward_impl(const uint8_t* x_codes, const float* x_scales, co
   const size_t ws_need = w_pre ? p.pre_w_offset() : p.ws_bytes();
   if (ws_need > 0 && (!workspace || ws_bytes < ws_need)) return HSQ_ERR_INVALID_ARG;
   if (p.kind == kGemv) {
-    hsq::GemvArgs ga{};
+    hsq::WithEpilogue<hsq::GemvArgs> ga{};
     ga.x_codes = x_codes; ga.x_scales = x_scales; ga.ldx = scales_ld(M);
     ga.w_codes = w_codes; ga.w_scales = w_scales; ga.ldw = scales_ld(N);
     ga.U = U; ga.r = r;
@@ -1340,7 +1343,7 @@ static hsq_status forward_impl(const uint8_t* x_codes, const float* x_scales, co
     return g128 ? launch_gemv<8, 4>(p, ga, stream) : launch_gemv<8, 2>(p, ga, stream);
   }
 
-  hsq::GemmArgs a{};
+  hsq::WithEpilogue<hsq::GemmArgs> a{};
   const int ldx = scales_ld(M), ldw = scales_ld(N);
   CUtensorMap tm_row, tm_col;
   bool ok;
@@ -1666,7 +1669,7 @@ hsq_status hsq_linear_forward_fused_ep(const void* X_bf16, const float* s, const
   p.kind = kGemv;
   p.tiles_r = gemv_rows_per_block(N, nsm);
   p.grid = (N + p.tiles_r - 1) / p.tiles_r;
-  hsq::GemvArgs ga{};
+  hsq::WithEpilogue<hsq::GemvArgs> ga{};
   ga.w_codes = w_codes; ga.w_scales = w_scales; ga.ldw = scales_ld(N);
   ga.r = r;
   ga.L2 = static_cast<const __nv_bfloat16*>(L2_bf16);
@@ -1997,7 +2000,7 @@ hsq_status hsq_fp4_linear_forward_ep(const uint8_t* x_codes, const uint8_t* x_sf
   if (!make_fp4_codes_map(&tm_a, x_codes, M, Kq, Cfg::BM) || !make_fp4_codes_map(&tm_b, w_codes, N, Kq, Cfg::BN) ||
       !make_y_map(&tm_y, Y, M, N, out == HSQ_OUT_F32))
     return HSQ_ERR_CUDA;
-  hsq::Fp4Args a{};
+  hsq::WithEpilogue<hsq::Fp4Args> a{};
   a.x_sf = x_sf; a.w_sf = w_sf; a.x_gs = x_gs; a.w_gs = w_gs;
   a.U = U;
   a.L2 = static_cast<const __nv_bfloat16*>(L2_bf16);
@@ -2025,9 +2028,13 @@ hsq_status hsq_fp4_linear_forward_ep(const uint8_t* x_codes, const uint8_t* x_sf
   }
   const int tiles = a.tiles_m * a.tiles_n;
   const int grid = std::min(tiles, device_sm_count());
-  if (launch_pdl(false, ep ? hsq::fp4_gemm_kernel<Cfg, true> : hsq::fp4_gemm_kernel<Cfg>, dim3(grid),
-                 dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream, tm_a, tm_b, tm_y, a) != cudaSuccess)
-    return HSQ_ERR_CUDA;
+  const hsq::Fp4Args& plain = a;
+  const cudaError_t e =
+      ep ? launch_pdl(false, hsq::fp4_gemm_kernel<Cfg, true>, dim3(grid), dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream,
+                      tm_a, tm_b, tm_y, a)
+         : launch_pdl(false, hsq::fp4_gemm_kernel<Cfg>, dim3(grid), dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream, tm_a,
+                      tm_b, tm_y, plain);
+  if (e != cudaSuccess) return HSQ_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? HSQ_OK : HSQ_ERR_CUDA;
 }
 
