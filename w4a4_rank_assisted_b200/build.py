@@ -45,11 +45,12 @@ def needs_build() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/hsq_lib.cu into w4a4_rank_assisted_b200/libhsq.so; returns its path."""
+    """Compile csrc/*.cu into w4a4_rank_assisted_b200/libhsq.so; returns its path."""
     if not force and not needs_build():
         return LIB_PATH
     tmp = LIB_PATH + ".tmp"
-    cmd = [_nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-o", tmp, os.path.join(CSRC, "hsq_lib.cu"), "-lcublas"]
+    units = [os.path.join(CSRC, f) for f in ("hsq_lib.cu", "hsq_heads.cu")]
+    cmd = [_nvcc(), *NVCC_FLAGS, "-t", "2", "-I", INCLUDE, "-o", tmp, *units, "-lcublas"]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd), file=sys.stderr)

@@ -13,9 +13,9 @@
 
 namespace hsq {
 
-// Device status word (one per device): bit 0 = a wait timed out, bit 1 = a cache
-// append met a page outside its cache.
-__device__ unsigned int g_status;
+// Device status word (one per device and translation unit): bit 0 = a wait timed
+// out, bit 1 = a cache append met a page outside its cache.
+static __device__ unsigned int g_status;
 
 constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusBadPage = 2u;
