@@ -563,10 +563,11 @@ hsq_status hsq_kv_append(const hsq_heads* k, const hsq_heads* v, const hsq_heads
 const char* hsq_status_string(hsq_status status);
 
 /*
- * Synchronizes `stream`, then reads and clears the device status word of the
- * current device: HSQ_ERR_TIMEOUT if any kernel since the last read gave up
- * waiting, else HSQ_ERR_BAD_PAGE if an hsq_kv_append met a page outside its cache,
- * HSQ_ERR_CUDA if the synchronization itself failed, else HSQ_OK.
+ * Synchronizes `stream`, then reads the current device's status and clears what it
+ * returns: HSQ_ERR_TIMEOUT if any kernel since that was last returned gave up
+ * waiting, else HSQ_ERR_BAD_PAGE if an hsq_kv_append since that was last returned met
+ * a page outside its cache, else HSQ_OK; HSQ_ERR_CUDA if the synchronization itself
+ * failed.  Where both happened, one call returns the first and the next the second.
  */
 hsq_status hsq_get_device_status(cudaStream_t stream);
 

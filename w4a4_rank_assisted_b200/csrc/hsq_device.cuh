@@ -13,8 +13,9 @@
 
 namespace hsq {
 
-// Device status word (one per device and translation unit): bit 0 = a wait timed
-// out, bit 1 = a cache append met a page outside its cache.
+// Device status word, one per device and translation unit: bit 0 = a wait timed out
+// (the linears' kernels), bit 1 = a cache append met a page outside its cache (the
+// head kernels, which wait for nothing).
 static __device__ unsigned int g_status;
 
 constexpr unsigned kStatusTimeout = 1u;

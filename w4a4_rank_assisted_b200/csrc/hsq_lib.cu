@@ -965,10 +965,12 @@ void hsq_debug_force_timeout(int flags, int limit_ms) {
 
 hsq_status hsq_get_device_status(cudaStream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return HSQ_ERR_CUDA;
-  unsigned v = 0, heads = 0;
-  if (take_status(&v) != cudaSuccess || hsq::take_heads_status(&heads) != cudaSuccess) return HSQ_ERR_CUDA;
-  v |= heads;
-  if (v) return (v & hsq::kStatusTimeout) ? HSQ_ERR_TIMEOUT : HSQ_ERR_BAD_PAGE;
+  // each word holds one kind: a bad page of the same interval stays for the next read
+  unsigned v = 0;
+  if (take_status(&v) != cudaSuccess) return HSQ_ERR_CUDA;
+  if (v) return HSQ_ERR_TIMEOUT;
+  if (hsq::take_heads_status(&v) != cudaSuccess) return HSQ_ERR_CUDA;
+  if (v) return HSQ_ERR_BAD_PAGE;
   return HSQ_OK;
 }
 
