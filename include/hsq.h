@@ -273,6 +273,8 @@ hsq_status hsq_linear_forward_noalloc(const uint8_t* x_codes, const float* x_sca
  *   X_bf16 [M][K] bf16, s [K] fp32, L1_bf16 [K][r] bf16 (NULL iff r == 0)
  *   w_codes/w_scales as written by hsq_pack_weights; L2_bf16, bias_bf16, Y, out
  *   as for hsq_linear_forward.  No workspace.
+ *   Y may not overlap X in form 1, whose blocks read X while others write Y
+ *   (HSQ_ERR_INVALID_ARG); form 2 has read X before it writes.
  */
 hsq_status hsq_linear_forward_fused(const void* X_bf16, const float* s, const void* L1_bf16,
                                     const uint8_t* w_codes, const float* w_scales,
@@ -297,8 +299,8 @@ hsq_status hsq_linear_forward_fused(const void* X_bf16, const float* s, const vo
  * may mul with mul_rows = 1; an operand that overlaps Y in any other way is
  * refused (HSQ_ERR_INVALID_ARG).  Y, and with it residual, may also be X in
  * hsq_linear_forward_x_ep (N == K); hsq_linear_forward_fused_ep refuses a Y that
- * overlaps X, which its blocks read while others write Y.  A NULL epilogue, or one that asks for nothing,
- * is the forward without it, bit for bit.
+ * overlaps X, in both of its forms.  A NULL epilogue, or one that asks for nothing,
+ * is the forward without it: the same bits, the same refusals.
  * The paper has no counterpart: in a transformer block these steps follow the
  * linear's output elementwise.
  *   hsq_linear_forward_ep          hsq_linear_forward, or hsq_linear_forward_pre

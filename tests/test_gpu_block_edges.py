@@ -4,13 +4,19 @@ gives, blocks that take several passes, objects that outlive what they were made
 import pytest
 import torch
 
-from test_gpu_block import packed
 from test_gpu_kv_append import Batch
 from w4a4_rank_assisted_b200 import hsq
+from w4a4_rank_assisted_b200.synth import LayerSpec, make_layer
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 BF = torch.bfloat16
+
+
+def packed(M, K, N, seed, group=64, r=4):
+    lay = make_layer(LayerSpec("e", M, K, N, r, act="outlier", outlier_frac=0.01, outlier_mult=5.0, seed=seed, group=group))
+    low = (None, None) if r == 0 else (lay.L1.to(DEV), lay.L2.to(DEV))
+    return hsq.PackedLinear(lay.W.to(DEV), torch.ones(K, device=DEV), *low, group=group)
 
 
 def test_a_timeout_and_a_bad_page_are_both_reported():
@@ -29,3 +35,22 @@ def test_a_timeout_and_a_bad_page_are_both_reported():
         assert hsq.hsq_get_device_status() == hsq.HSQ_ERR_TIMEOUT
         assert hsq.hsq_get_device_status() == hsq.HSQ_ERR_BAD_PAGE
         assert hsq.hsq_get_device_status() == hsq.HSQ_OK
+
+
+@pytest.mark.parametrize("M,K,r,group", [(5, 256, 4, 64), (16, 1152, 0, 64), (16, 2048, 4, 128), (3, 512, 8, 64)])
+def test_the_decode_tile_form_takes_y_over_x(M, K, r, group):
+    """Its grid barrier stands between the last read of X and the first write of Y: without an epilogue, or with one
+    that asks for nothing, the bits of a Y of its own; with one it refuses."""
+    layer = packed(M, K, K, M, group, r=r)
+    assert hsq.hsq_fused_form(M, K, K, r, group) == 2
+    x = torch.randn(M, K, device=DEV).to(BF)
+    want = torch.empty_like(x)
+    hsq.forward_fused(layer, x, want)
+    for ep in (None, hsq.Epilogue()):
+        for _ in range(5):
+            y = x.clone()
+            hsq.forward_fused(layer, y, y, epilogue=ep)
+            assert torch.equal(y, want)
+    with pytest.raises(hsq.HsqError):
+        hsq.forward_fused(layer, x, x, epilogue=hsq.Epilogue("relu"))
+    assert hsq.hsq_get_device_status() == hsq.HSQ_OK

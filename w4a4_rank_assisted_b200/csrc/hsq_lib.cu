@@ -1455,11 +1455,13 @@ hsq_status hsq_linear_forward_fused_ep(const void* X_bf16, const float* s, const
   // tokens: the decode tiles, the step spread over the grid
   const int form = fused_form(M, N, K, r, group, nsm);
   if (form == 0) return HSQ_ERR_UNSUPPORTED;
-  // every block reads X while others already write Y
-  if (ep && ranges_meet(X_bf16, static_cast<size_t>(M) * K * 2, Y, static_cast<size_t>(M) * N * (out == HSQ_OUT_F32 ? 4 : 2)))
-    return HSQ_ERR_INVALID_ARG;
   st = check_epilogue(&ep, M, N, Y, out);
   if (st != HSQ_OK) return st;
+  // form 1: every block reads X while others already write Y; form 2 writes Y behind
+  // the grid barrier that follows the last read of X
+  if ((form == 1 || ep) &&
+      ranges_meet(X_bf16, static_cast<size_t>(M) * K * 2, Y, static_cast<size_t>(M) * N * (out == HSQ_OUT_F32 ? 4 : 2)))
+    return HSQ_ERR_INVALID_ARG;
   if (form == 2)
     return forward_fused_dec16(X_bf16, s, L1_bf16, w_codes, w_scales, L2_bf16, bias_bf16, M, N, K, r, group, Y, out,
                                ep, stream);
