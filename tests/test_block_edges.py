@@ -3,6 +3,7 @@ devices that are refused before anything is launched, and the binding's objects.
 import ctypes
 
 import pytest
+import torch
 
 from w4a4_rank_assisted_b200 import hsq
 
@@ -22,3 +23,111 @@ def test_the_stream_form_refuses_y_over_x(M, r, group, shift):
     assert lib.hsq_linear_forward_fused_ep(*args, None, None) == INVALID
     assert lib.hsq_linear_forward_fused_ep(*args, ctypes.byref(hsq._CEpilogue()), None) == INVALID
     assert lib.hsq_linear_forward_fused_ep(*args, ctypes.byref(hsq._CEpilogue(act=4)), None) == INVALID
+
+
+class FakeTensor:
+    """What the binding asks of a CUDA tensor, without a GPU."""
+
+    is_cuda = True
+
+    def __init__(self, device, *shape, dtype=torch.bfloat16):
+        self.device_index, self.shape, self.dtype = device, torch.Size(shape), dtype
+
+    def get_device(self):
+        return self.device_index
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.shape.numel()
+
+    def data_ptr(self):
+        return FAR
+
+
+class FakeLibrary:
+    """Records every call with the device that is current during it."""
+
+    def __init__(self, current):
+        self.calls, self.current = [], current
+
+    def __getattr__(self, name):
+        return lambda *a: self.calls.append((name, self.current[-1], a[-1])) or 0
+
+
+@pytest.fixture
+def library(monkeypatch):
+    """The fake library with device 0 current; device d's current stream is 100 + d."""
+    current = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *e):
+            current.pop()
+
+    lib = FakeLibrary(current)
+    monkeypatch.setattr(hsq, "load", lambda *a: lib)
+    monkeypatch.setattr(hsq, "_raw_stream", lambda d: 100 + d)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    return lib
+
+
+def _tensors(device, names):
+    return {n: FakeTensor(device, 16, 64) for n in names}
+
+
+CALLS = {
+    "hsq_linear_forward_ep": ("x_codes", "x_scales", "U", "w_codes", "w_scales", "w_e4m3", "L2", "bias", "workspace"),
+    "hsq_linear_forward_noalloc_ep": ("x_codes", "x_scales", "U", "w_codes", "w_scales", "L2", "bias"),
+    "hsq_linear_forward_x_ep": ("X", "s", "L1", "w_codes", "w_scales", "w_e4m3", "L2", "bias", "workspace"),
+    "hsq_linear_forward_fused_ep": ("X", "s", "L1", "w_codes", "w_scales", "L2", "bias"),
+    "hsq_fp4_linear_forward_ep": ("x_codes", "x_sf", "x_gs", "U", "w_codes", "w_sf", "w_gs", "L2", "bias"),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_every_tensor_of_a_forward_lives_on_its_device(name, library):
+    """One tensor on another GPU refuses the call; all of them on another GPU than the current one run there."""
+    call = getattr(hsq, name)
+    dims = dict(M=16, N=64, K=64, r=4)
+    for other in CALLS[name]:
+        t = _tensors(0, CALLS[name])
+        t[other] = FakeTensor(1, 16, 64)
+        with pytest.raises(ValueError, match="device"):
+            call(Y=FakeTensor(0, 16, 64), epilogue=None, **t, **dims)
+    assert not library.calls
+    call(Y=FakeTensor(1, 16, 64), epilogue=None, **_tensors(1, CALLS[name]), **dims)
+    assert library.calls == [(name, 1, 101)]
+
+
+class Parts:
+    def __init__(self, device, **kw):
+        self.__dict__.update(_tensors(device, ("w_codes", "w_scales", "w_e4m3", "L1", "L2", "bias", "s", "w_sf", "w_gs",
+                                               "x_codes", "x_scales", "x_sf", "x_gs", "U")), N=64, K=64, r=4, group=64, **kw)
+
+
+@pytest.mark.parametrize("fp4", [False, True], ids=["int4", "nvfp4"])
+def test_both_steps_of_a_forward_run_on_its_tensors_device(fp4, library):
+    """With an epilogue the activation step, too, runs on the tensors' device, and is not launched where the forward
+    would be refused."""
+    f = hsq.fp4_forward if fp4 else hsq.forward
+    names = ["hsq_fp4_quantize_act", "hsq_fp4_linear_forward_ep"] if fp4 else ["hsq_quantize_act", "hsq_linear_forward_ep"]
+    f(Parts(1), FakeTensor(1, 16, 64), Parts(1), FakeTensor(1, 16, 64), epilogue=hsq.Epilogue("silu"))
+    assert [c[:2] for c in library.calls] == [(n, 1) for n in names] and {c[2] for c in library.calls} == {101}
+    library.calls.clear()
+    f(Parts(1), FakeTensor(1, 16, 64), Parts(1), FakeTensor(1, 16, 64), epilogue=hsq.Epilogue("silu"), stream=7)
+    assert [c[1:] for c in library.calls] == [(1, 7)] * 2
+    library.calls.clear()
+    for X, Y, layer, act in ((0, 1, 1, 1), (1, 0, 1, 1), (1, 1, 0, 1), (1, 1, 1, 0)):
+        with pytest.raises(ValueError, match="device"):
+            f(Parts(layer), FakeTensor(X, 16, 64), Parts(act), FakeTensor(Y, 16, 64), epilogue=hsq.Epilogue("silu"))
+    with pytest.raises(ValueError):
+        f(Parts(1), FakeTensor(1, 16, 64), Parts(1), FakeTensor(1, 16, 72), epilogue=hsq.Epilogue("silu"))
+    assert not library.calls

@@ -368,7 +368,7 @@ def hsq_linear_forward_ep(x_codes, x_scales, U, w_codes, w_scales, w_e4m3, L2, b
                           epilogue: Optional[Epilogue], out: int = HSQ_OUT_BF16, workspace=None, ws_bytes: int = 0,
                           group=GROUP, stream=None) -> None:
     """hsq_linear_forward (w_e4m3 None) or hsq_linear_forward_pre with an epilogue."""
-    ep = _ep(epilogue, Y, M, N, out, x_codes, w_codes, w_e4m3, workspace)
+    ep = _ep(epilogue, Y, M, N, out, x_codes, x_scales, U, w_codes, w_scales, w_e4m3, L2, bias, workspace)
     _check(_on_device(Y.get_device(), stream, lambda s: load().hsq_linear_forward_ep(
         _ptr(x_codes), _ptr(x_scales), _ptr(U), _ptr(w_codes), _ptr(w_scales), _ptr(w_e4m3), _ptr(L2), _ptr(bias), M, N,
         K, r, group, _ptr(Y), int(out), ep, _ptr(workspace), int(ws_bytes), s)), "hsq_linear_forward_ep")
@@ -378,7 +378,7 @@ def hsq_linear_forward_noalloc_ep(x_codes, x_scales, U, w_codes, w_scales, L2, b
                                   epilogue: Optional[Epilogue], out: int = HSQ_OUT_BF16, group=GROUP,
                                   stream=None) -> None:
     """hsq_linear_forward_noalloc with an epilogue."""
-    ep = _ep(epilogue, Y, M, N, out, x_codes, w_codes)
+    ep = _ep(epilogue, Y, M, N, out, x_codes, x_scales, U, w_codes, w_scales, L2, bias)
     _check(_on_device(Y.get_device(), stream, lambda s: load().hsq_linear_forward_noalloc_ep(
         _ptr(x_codes), _ptr(x_scales), _ptr(U), _ptr(w_codes), _ptr(w_scales), _ptr(L2), _ptr(bias), M, N, K, r, group,
         _ptr(Y), int(out), ep, s)), "hsq_linear_forward_noalloc_ep")
@@ -388,7 +388,7 @@ def hsq_linear_forward_x_ep(X, s, L1, w_codes, w_scales, w_e4m3, L2, bias, M, N,
                             epilogue: Optional[Epilogue], out: int = HSQ_OUT_BF16, workspace=None, ws_bytes: int = 0,
                             group=GROUP, stream=None) -> None:
     """hsq_linear_forward_x with an epilogue."""
-    ep = _ep(epilogue, Y, M, N, out, X, w_codes, w_e4m3, workspace)
+    ep = _ep(epilogue, Y, M, N, out, X, s, L1, w_codes, w_scales, w_e4m3, L2, bias, workspace)
     _check(_on_device(Y.get_device(), stream, lambda st: load().hsq_linear_forward_x_ep(
         _ptr(X), _ptr(s), _ptr(L1), _ptr(w_codes), _ptr(w_scales), _ptr(w_e4m3), _ptr(L2), _ptr(bias), M, N, K, r, group,
         _ptr(Y), int(out), ep, _ptr(workspace), int(ws_bytes), st)), "hsq_linear_forward_x_ep")
@@ -397,7 +397,7 @@ def hsq_linear_forward_x_ep(X, s, L1, w_codes, w_scales, w_e4m3, L2, bias, M, N,
 def hsq_linear_forward_fused_ep(X, s, L1, w_codes, w_scales, L2, bias, M, N, K, r, Y, epilogue: Optional[Epilogue],
                                 out: int = HSQ_OUT_BF16, group=GROUP, stream=None) -> None:
     """hsq_linear_forward_fused with an epilogue."""
-    ep = _ep(epilogue, Y, M, N, out, X, w_codes)
+    ep = _ep(epilogue, Y, M, N, out, X, s, L1, w_codes, w_scales, L2, bias)
     _check(_on_device(Y.get_device(), stream, lambda st: load().hsq_linear_forward_fused_ep(
         _ptr(X), _ptr(s), _ptr(L1), _ptr(w_codes), _ptr(w_scales), _ptr(L2), _ptr(bias), M, N, K, r, group, _ptr(Y),
         int(out), ep, st)), "hsq_linear_forward_fused_ep")
@@ -406,7 +406,7 @@ def hsq_linear_forward_fused_ep(X, s, L1, w_codes, w_scales, L2, bias, M, N, K, 
 def hsq_fp4_linear_forward_ep(x_codes, x_sf, x_gs, U, w_codes, w_sf, w_gs, L2, bias, M, N, K, r, Y,
                               epilogue: Optional[Epilogue], out: int = HSQ_OUT_BF16, stream=None) -> None:
     """hsq_fp4_linear_forward with an epilogue."""
-    ep = _ep(epilogue, Y, M, N, out, x_codes, w_codes)
+    ep = _ep(epilogue, Y, M, N, out, x_codes, x_sf, x_gs, U, w_codes, w_sf, w_gs, L2, bias)
     _check(_on_device(Y.get_device(), stream, lambda s: load().hsq_fp4_linear_forward_ep(
         _ptr(x_codes), _ptr(x_sf), _ptr(x_gs), _ptr(U), _ptr(w_codes), _ptr(w_sf), _ptr(w_gs), _ptr(L2), _ptr(bias), M,
         N, K, r, _ptr(Y), int(out), ep, s)), "hsq_fp4_linear_forward_ep")
@@ -790,14 +790,22 @@ def forward(layer: PackedLinear, X: torch.Tensor, act: ActBuffers, Y: torch.Tens
     M = X.shape[0]
     if act.group != layer.group:
         raise ValueError("activation buffers and packed layer use different group sizes")
-    hsq_quantize_act(X, layer.s, layer.L1, M, layer.K, layer.r, act.x_codes, act.x_scales, act.U,
-                     group=layer.group, stream=stream)
     ws_bytes = 0 if workspace is None else workspace.numel()
     if epilogue is not None:
-        hsq_linear_forward_ep(act.x_codes, act.x_scales, act.U, layer.w_codes, layer.w_scales, layer.w_e4m3,
-                              layer.L2, layer.bias, M, layer.N, layer.K, layer.r, Y, epilogue, out=out,
-                              workspace=workspace, ws_bytes=ws_bytes, group=layer.group, stream=stream)
-    elif layer.w_e4m3 is not None:
+        _ep(epilogue, Y, M, layer.N, out, X, layer.s, layer.L1, act.x_codes, act.x_scales, act.U)
+
+        def both(st):  # on the tensors' device
+            hsq_quantize_act(X, layer.s, layer.L1, M, layer.K, layer.r, act.x_codes, act.x_scales, act.U,
+                             group=layer.group, stream=st)
+            hsq_linear_forward_ep(act.x_codes, act.x_scales, act.U, layer.w_codes, layer.w_scales, layer.w_e4m3,
+                                  layer.L2, layer.bias, M, layer.N, layer.K, layer.r, Y, epilogue, out=out,
+                                  workspace=workspace, ws_bytes=ws_bytes, group=layer.group, stream=st)
+
+        _on_device(Y.get_device(), stream, both)
+        return Y
+    hsq_quantize_act(X, layer.s, layer.L1, M, layer.K, layer.r, act.x_codes, act.x_scales, act.U,
+                     group=layer.group, stream=stream)
+    if layer.w_e4m3 is not None:
         hsq_linear_forward_pre(act.x_codes, act.x_scales, act.U, layer.w_codes, layer.w_scales, layer.w_e4m3,
                                layer.L2, layer.bias, M, layer.N, layer.K, layer.r, Y, out=out, workspace=workspace,
                                ws_bytes=ws_bytes, group=layer.group, stream=stream)
@@ -878,13 +886,19 @@ def fp4_forward(layer: Fp4Linear, X: torch.Tensor, act: Fp4ActBuffers, Y: torch.
     """One NVFP4 forward: the activation step, then the block-scaled GEMM + epilogue
     (U L2 + bias, and where one is given act, mul and residual)."""
     M = X.shape[0]
+    if epilogue is not None:
+        _ep(epilogue, Y, M, layer.N, out, X, layer.s, layer.L1, act.x_codes, act.x_sf, act.x_gs, act.U)
+
+        def both(st):  # on the tensors' device
+            hsq_fp4_quantize_act(X, layer.s, layer.L1, M, layer.K, layer.r, act.x_codes, act.x_sf, act.x_gs, act.U,
+                                 stream=st)
+            hsq_fp4_linear_forward_ep(act.x_codes, act.x_sf, act.x_gs, act.U, layer.w_codes, layer.w_sf, layer.w_gs,
+                                      layer.L2, layer.bias, M, layer.N, layer.K, layer.r, Y, epilogue, out=out, stream=st)
+
+        _on_device(Y.get_device(), stream, both)
+        return Y
     hsq_fp4_quantize_act(X, layer.s, layer.L1, M, layer.K, layer.r, act.x_codes, act.x_sf, act.x_gs, act.U,
                          stream=stream)
-    if epilogue is not None:
-        hsq_fp4_linear_forward_ep(act.x_codes, act.x_sf, act.x_gs, act.U, layer.w_codes, layer.w_sf, layer.w_gs,
-                                  layer.L2, layer.bias, M, layer.N, layer.K, layer.r, Y, epilogue, out=out,
-                                  stream=stream)
-        return Y
     hsq_fp4_linear_forward(act.x_codes, act.x_sf, act.x_gs, act.U, layer.w_codes, layer.w_sf, layer.w_gs,
                            layer.L2, layer.bias, M, layer.N, layer.K, layer.r, Y, out=out, stream=stream)
     return Y
