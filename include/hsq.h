@@ -466,8 +466,11 @@ hsq_status hsq_fp4_linear_forward_ep(const uint8_t* x_codes, const uint8_t* x_sf
  * products and sums are fp32, with one rounding to the output type.
  *
  * Pointers of these two calls need the alignment of their element type only;
- * 16-byte aligned rows are faster.  Host structs are read during the call and may
- * be reused afterwards.
+ * 16-byte aligned rows are faster.  At most 65536 heads of a kind; an append of more
+ * than 131070 query, key and value heads together returns HSQ_ERR_UNSUPPORTED where
+ * its heads have more than 128 pieces (a piece: 16 or 8 bytes of input, or an element
+ * where the layout allows neither; two pieces of pairs count once).  Host structs are
+ * read during the call and may be reused afterwards.
  */
 #define HSQ_ROPE_MAX_AXES 4
 

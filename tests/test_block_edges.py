@@ -131,3 +131,22 @@ def test_both_steps_of_a_forward_run_on_its_tensors_device(fp4, library):
     with pytest.raises(ValueError):
         f(Parts(1), FakeTensor(1, 16, 64), Parts(1), FakeTensor(1, 16, 72), epilogue=hsq.Epilogue("silu"))
     assert not library.calls
+
+
+def test_append_refuses_more_head_blocks_than_a_grid_holds():
+    """196608 heads of 447 single elements' units: refused as an argument, not by the launch.  65537 of a kind: never
+    taken."""
+    far, ref, H = 1 << 44, ctypes.byref, 65536
+
+    def append(q_heads, kv, dim=511):
+        at = lambda i: hsq._CHeads((i + 1) * far, H * dim, dim)  # noqa: E731
+        cache = hsq._CPagedCache(k=5 * far, v=6 * far, dtype=0, pages=2, page_size=4, page_stride=4 * H * dim,
+                                 slot_stride=H * dim, head_stride=dim)
+        seqs = hsq._CSequences(block_table=7 * far, cache_lens=8 * far, cu_seqlens=None, count=1, max_pages=2, table_ld=2)
+        rot = hsq._CRotation(freqs=9 * far, pair_axis=None, pairs=64, n_axes=1, scale=1.0)
+        return hsq.load().hsq_kv_append(ref(at(0)), ref(at(1)), ref(at(2)), ref(at(3)), 0, 1, q_heads, kv, dim, ref(rot),
+                                        None, ref(cache), ref(seqs), None)
+
+    assert append(H, H) == hsq.HSQ_ERR_UNSUPPORTED
+    assert append(1, H) == hsq.HSQ_ERR_UNSUPPORTED  # 131073 heads, 65537 blocks
+    assert append(H + 1, 1) == INVALID and append(1, H + 1) == INVALID

@@ -54,3 +54,16 @@ def test_the_decode_tile_form_takes_y_over_x(M, K, r, group):
     with pytest.raises(hsq.HsqError):
         hsq.forward_fused(layer, x, x, epilogue=hsq.Epilogue("relu"))
     assert hsq.hsq_get_device_status() == hsq.HSQ_OK
+
+
+def test_append_of_as_many_head_blocks_as_a_grid_holds():
+    """65534 + 2 * 32768 heads of single elements: 65535 blocks.  Position 0 turns nothing, so all is copied."""
+    q, kv, D = 65534, 32768, 511
+    qkv = torch.randn(1, q + 2 * kv, D, device=DEV).to(BF)
+    kc, vc = torch.zeros(1, 1, kv, D, device=DEV, dtype=BF), torch.zeros(1, 1, kv, D, device=DEV, dtype=BF)
+    qo = torch.zeros(1, q, D, device=DEV, dtype=BF)
+    zero = torch.zeros(1, dtype=torch.int32, device=DEV)
+    hsq.hsq_kv_append(qkv[:, q:q + kv], qkv[:, q + kv:], kc, vc, zero[None], zero, q=qkv[:, :q], q_out=qo,
+                      rotation=hsq.Rotation(torch.ones(64, device=DEV)))
+    assert torch.equal(qo, qkv[:, :q]) and torch.equal(kc[0, 0], qkv[0, q:q + kv]) and torch.equal(vc[0, 0], qkv[0, q + kv:])
+    assert hsq.hsq_get_device_status() == hsq.HSQ_OK

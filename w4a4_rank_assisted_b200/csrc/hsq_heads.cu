@@ -146,10 +146,16 @@ hsq::RopeGrid rope_grid(int tokens, int units, int heads, int pairs) {
   return g;
 }
 
+// Blocks along the heads, in the grid's y dimension, which holds 65535 (above that only
+// with more than 131070 heads of more than 128 units: a thread row to a head).
+int head_blocks(const hsq::RopeGrid& g, int heads) {
+  return (heads + g.splits * hsq::kRopeHeads - 1) / (g.splits * hsq::kRopeHeads);
+}
+
 template <class Args>
 cudaError_t launch_heads(void (*kernel)(Args), const Args& a, int heads, size_t smem, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>((a.tokens + static_cast<long long>(a.g.tokens) * a.g.passes - 1) / (a.g.tokens * a.g.passes)),
-                  static_cast<unsigned>((heads + a.g.splits * hsq::kRopeHeads - 1) / (a.g.splits * hsq::kRopeHeads)));
+                  static_cast<unsigned>(head_blocks(a.g, heads)));
   const int threads = (a.g.lanes * a.g.splits * a.g.tokens + 31) / 32 * 32;
   return launch_pdl(true, kernel, grid, dim3(threads), smem, st, a);
 }
@@ -324,6 +330,7 @@ hsq_status hsq_kv_append(const hsq_heads* k, const hsq_heads* v, const hsq_heads
   const int pairs = rot ? rot->pairs : 0;
   const int w = piece_width(dtype, head_dim, pairs, bits);
   a.g = rope_grid(tokens, pairs / w + (head_dim - 2 * pairs) / w, q_heads + 2 * kv_heads, pairs);
+  if (head_blocks(a.g, q_heads + 2 * kv_heads) > 65535) return HSQ_ERR_UNSUPPORTED;
   const bool adj = rot && rot->interleaved;
   cudaError_t e;
   if (dtype == HSQ_BF16)
