@@ -10,7 +10,7 @@ from w4a4_rank_assisted_b200.synth import LayerSpec, make_layer
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
-BF = torch.bfloat16
+BF, F32 = torch.bfloat16, torch.float32
 
 
 def packed(M, K, N, seed, group=64, r=4):
@@ -67,3 +67,62 @@ def test_append_of_as_many_head_blocks_as_a_grid_holds():
                       rotation=hsq.Rotation(torch.ones(64, device=DEV)))
     assert torch.equal(qo, qkv[:, :q]) and torch.equal(kc[0, 0], qkv[0, q:q + kv]) and torch.equal(vc[0, 0], qkv[0, q + kv:])
     assert hsq.hsq_get_device_status() == hsq.HSQ_OK
+
+
+def _nans(t, seed):
+    """Fill a bf16 or fp32 tensor with bit patterns, NaN of every kind among them (an integer view writes them)."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    bits = t.view(torch.int16 if t.dtype == BF else torch.int32)
+    bits.copy_(torch.randint(-(1 << 15), 1 << 15, t.shape, generator=g, device=DEV) if t.dtype == BF
+               else torch.randint(-(1 << 31), 1 << 31, t.shape, generator=g, device=DEV))
+    some = ([0x7FC1, 0xFF81 - 0x10000, 0x7F81, -1, 0x7FFF, 0x7F80, 0xFF80 - 0x10000] if t.dtype == BF else
+            [0x7FC00001, 0x7F800001, -1, 0x7F800000, -(1 << 23)])
+    bits[..., :len(some)] = torch.tensor(some, device=DEV, dtype=bits.dtype)
+    bits[..., -len(some):] = torch.tensor(some, device=DEV, dtype=bits.dtype)
+    return t
+
+
+def _same_bits(a, b):
+    kind = {2: torch.int16, 4: torch.int32}[a.element_size()]
+    return torch.equal(a.contiguous().view(kind), b.contiguous().view(kind))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D,pairs,off", [(64, 16, 0), (72, 4, 0), (64, 16, 1), (31, 7, 0)],
+                         ids=["16-byte", "8-byte", "off", "odd"])
+@pytest.mark.parametrize("adjacent", [False, True], ids=["halves", "adjacent"])
+def test_what_is_only_moved_keeps_its_bits(dtype, D, pairs, off, adjacent):
+    """Elements behind the pairs, values, and heads without a rotation are copied bit for bit, every NaN's sign and
+    payload included, in place and out of place, in pieces of any width."""
+    T, q, kv, page = 9, 4, 2, 4
+    n = T * (q + 2 * kv) * D
+    qkv = _nans(torch.empty(n + 8, device=DEV, dtype=dtype)[off:n + off].view(T, q + 2 * kv, D), D)
+    freqs = torch.linspace(1.0, 0.1, pairs, device=DEV)
+    rot, pos = hsq.Rotation(freqs, interleaved=adjacent), torch.arange(T, device=DEV)
+    x, y = qkv[:, :q], torch.zeros(T, q, D, device=DEV, dtype=dtype)
+    hsq.hsq_rope(x, y, pos, rot)
+    assert _same_bits(y[..., 2 * pairs:], x[..., 2 * pairs:])
+    w = qkv.clone()
+    hsq.hsq_rope(w[:, :q], w[:, :q], pos, rot)
+    assert _same_bits(w[..., 2 * pairs:], qkv[..., 2 * pairs:]) and _same_bits(w[:, q:], qkv[:, q:])
+    table = torch.tensor([[2, 0, 3]], dtype=torch.int32, device=DEV)
+    zero = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    at = torch.arange(T, device=DEV)
+    pages, slots = table[0, at // page].long(), at % page
+    k, v = qkv[:, q:q + kv], qkv[:, q + kv:]
+    for r in (rot, None):
+        p = 0 if r is None else 2 * pairs
+        kc, vc = (torch.zeros(4, page, kv, D, device=DEV, dtype=dtype) for _ in range(2))
+        qo = torch.zeros(T, q, D, device=DEV, dtype=dtype)
+        hsq.hsq_kv_append(k, v, kc, vc, table, zero, cu_seqlens=cu, rotation=r, q=x, q_out=qo)
+        assert _same_bits(vc[pages, slots], v)
+        assert _same_bits(kc[pages, slots][..., p:], k[..., p:]) and _same_bits(qo[..., p:], x[..., p:])
+        w = qkv.clone()
+        hsq.hsq_kv_append(w[:, q:q + kv], w[:, q + kv:], kc, vc, table, zero, cu_seqlens=cu, rotation=r, q=w[:, :q],
+                          q_out=w[:, :q])
+        assert _same_bits(w[..., p:], qkv[..., p:]) and _same_bits(w[:, q:], qkv[:, q:])
+    if dtype == BF:  # a wider cache holds the same NaN: its upper half
+        vc = torch.zeros(4, page, kv, D, device=DEV)
+        hsq.hsq_kv_append(k, v, vc.clone(), vc, table, zero, cu_seqlens=cu)
+        assert torch.equal(vc[pages, slots].contiguous().view(torch.int32) >> 16, v.contiguous().view(torch.int16).int())

@@ -24,6 +24,8 @@
 // turns, is rounded to fp32 for sincospi.
 #pragma once
 
+#include <type_traits>
+
 #include "hsq_device.cuh"
 
 namespace hsq {
@@ -73,13 +75,18 @@ __device__ __forceinline__ void rope_angle(const RopeTable& t, int i, size_t row
   s *= t.scale * t.sign;
 }
 
-// V consecutive elements of a head as loaded (one access), and as fp32.
+// V consecutive elements of a head as loaded (one access), and as fp32.  What is only
+// moved is stored as loaded: through fp32 a bf16 NaN would lose its sign and payload.
 template <typename T, int V>
 struct Piece {
   uint32_t w[V * sizeof(T) / 4];
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (sizeof(w) == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
     else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (sizeof(w) == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
+    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(w);
   }
   __device__ __forceinline__ float at(int j) const {
     if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
@@ -90,6 +97,7 @@ template <typename T>
 struct Piece<T, 1> {
   T x;
   __device__ __forceinline__ void load(const T* p) { x = *p; }
+  __device__ __forceinline__ void store(T* p) const { *p = x; }
   __device__ __forceinline__ float at(int) const { return static_cast<float>(x); }
 };
 
@@ -290,17 +298,19 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 4 : 3) rope_ker
 #pragma unroll
     for (int i = 0; i < kRopeHeads; ++i) {
       if (h0 + i >= a.heads) break;
-      float f[V], g[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        f[j] = pc[i].at(j);
-        g[j] = qc[i].at(j);
-      }
       if (now.b >= 0) {
+        float f[V], g[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          f[j] = pc[i].at(j);
+          g[j] = qc[i].at(j);
+        }
         RopeUnit<V, ADJ>::rotate(f, g, c, s);
         store_piece<V>(yk + now.b, g);
+        store_piece<V>(yk + now.a, f);
+      } else {
+        pc[i].store(yk + now.a);
       }
-      store_piece<V>(yk + now.a, f);
       yk += a.y.hs;
     }
   }
@@ -433,34 +443,59 @@ __global__ void __launch_bounds__(kRopeThreads, 3) kv_append_kernel(const __grid
     for (int i = 0; i < kRopeHeads; ++i) {
       const int e = h0 + i;
       if (e >= nh) break;
-      float f[V], g[V];
+      const bool turned = un.b >= 0 && e < nr, is_q = e < a.q_heads, is_k = !is_q && e < nr;
+      const int hd = e - (is_q ? 0 : is_k ? a.q_heads : nr);
+      auto q_row = [&] { return static_cast<T*>(a.q_out.data) + tok * a.q_out.ts + hd * a.q_out.hs; };
+      auto cache_row = [&](const CacheView& cv) {
+        return static_cast<C*>(cv.data) + me.page * cv.ps + me.slot * cv.ss + hd * cv.hs;
+      };
+      auto values = [&](float (&f)[V], float (&g)[V]) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        f[j] = pc[i].at(j);
-        g[j] = qc[i].at(j);
-      }
-      if (un.b >= 0 && e < nr) RopeUnit<V, ADJ>::rotate(f, g, c, s);
-      if (e < a.q_heads) {
-        T* y = static_cast<T*>(a.q_out.data) + tok * a.q_out.ts + e * a.q_out.hs;
-        if (un.b >= 0) store_piece<V>(y + un.b, g);
-        if (un.b >= 0 || !a.q_in_place) store_piece<V>(y + un.a, f);
-      } else if (me.page >= 0) {
-        const bool is_k = e < nr;
-        const CacheView& cv = is_k ? a.kc : a.vc;
-        const int hd = e - (is_k ? a.q_heads : nr);
-        C* y = static_cast<C*>(cv.data) + me.page * cv.ps + me.slot * cv.ss + hd * cv.hs;
-        if constexpr (sizeof(C) == 1) {
-          if (cv.scale) {
-            const float sc = __ldg(cv.scale + hd);
+        for (int j = 0; j < V; ++j) {
+          f[j] = pc[i].at(j);
+          g[j] = qc[i].at(j);
+        }
+        if (turned) RopeUnit<V, ADJ>::rotate(f, g, c, s);
+      };
+      if constexpr (std::is_same_v<T, C>) {
+        if (!is_q && me.page < 0) continue;
+        T* y = is_q ? q_row() : cache_row(is_k ? a.kc : a.vc);
+        if (turned) {
+          float f[V], g[V];
+          values(f, g);
+          store_piece<V>(y + un.a, f);
+          store_piece<V>(y + un.b, g);
+        } else {
+          if (!is_q || !a.q_in_place) pc[i].store(y + un.a);
+          if (un.b >= 0) qc[i].store(y + un.b);
+        }
+      } else {
+        float f[V], g[V];
+        values(f, g);
+        if (is_q) {
+          T* y = q_row();
+          if (turned) {
+            store_piece<V>(y + un.b, g);
+            store_piece<V>(y + un.a, f);
+          } else if (!a.q_in_place) {
+            pc[i].store(y + un.a);
+          }
+        } else if (me.page >= 0) {
+          const CacheView& cv = is_k ? a.kc : a.vc;
+          C* y = cache_row(cv);
+          if constexpr (sizeof(C) == 1) {
+            if (cv.scale) {
+              const float sc = __ldg(cv.scale + hd);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-              f[j] = __fdiv_rn(f[j], sc);
-              g[j] = __fdiv_rn(g[j], sc);
+              for (int j = 0; j < V; ++j) {
+                f[j] = __fdiv_rn(f[j], sc);
+                g[j] = __fdiv_rn(g[j], sc);
+              }
             }
           }
+          store_piece<V>(y + un.a, f);
+          if (un.b >= 0) store_piece<V>(y + un.b, g);
         }
-        store_piece<V>(y + un.a, f);
-        if (un.b >= 0) store_piece<V>(y + un.b, g);
       }
     }
   }
