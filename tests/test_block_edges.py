@@ -150,3 +150,17 @@ def test_append_refuses_more_head_blocks_than_a_grid_holds():
     assert append(H, H) == hsq.HSQ_ERR_UNSUPPORTED
     assert append(1, H) == hsq.HSQ_ERR_UNSUPPORTED  # 131073 heads, 65537 blocks
     assert append(H + 1, 1) == INVALID and append(1, H + 1) == INVALID
+
+
+def test_a_decode_step_of_no_sequences_does_nothing():
+    """One new token per sequence and no sequence: tokens == count == 0."""
+    ref = ctypes.byref
+    heads = hsq._CHeads(None, 512, 128)
+    cache = hsq._CPagedCache(k=A, v=FAR, dtype=0, pages=2, page_size=4, page_stride=4 * 512, slot_stride=512, head_stride=128)
+    call = lambda tokens, **kw: hsq.load().hsq_kv_append(  # noqa: E731
+        ref(heads), ref(heads), None, None, 0, tokens, 0, 4, 128, None, None, ref(cache),
+        ref(hsq._CSequences(**{**dict(count=0, max_pages=2, table_ld=2), **kw})), None)
+    assert call(0) == hsq.HSQ_OK
+    assert call(0, count=-1) == INVALID
+    assert call(1) == INVALID
+    assert call(0, cu_seqlens=A) == INVALID  # cu_seqlens of no sequence

@@ -234,7 +234,9 @@ hsq_status hsq_kv_append(const hsq_heads* k, const hsq_heads* v, const hsq_heads
   if (rot && (st = check_rotation(rot, head_dim)) != HSQ_OK) return st;
   if (cache->dtype != HSQ_BF16 && cache->dtype != HSQ_F32 && cache->dtype != HSQ_E4M3) return HSQ_ERR_INVALID_ARG;
   if (cache->dtype != HSQ_E4M3 && (cache->k_scale || cache->v_scale)) return HSQ_ERR_INVALID_ARG;
-  if (cache->pages < 1 || cache->page_size < 1 || seqs->count < 1 || seqs->max_pages < 1) return HSQ_ERR_INVALID_ARG;
+  // (one new token per sequence: none where there are no sequences)
+  if (cache->pages < 1 || cache->page_size < 1 || seqs->max_pages < 1) return HSQ_ERR_INVALID_ARG;
+  if (seqs->count < (!seqs->cu_seqlens && tokens == 0 ? 0 : 1)) return HSQ_ERR_INVALID_ARG;
   if (tokens == 0) return HSQ_OK;
   if (!cache->k || !cache->v || !seqs->block_table || !seqs->cache_lens) return HSQ_ERR_INVALID_ARG;
   if (seqs->table_ld < seqs->max_pages || seqs->table_ld > kMaxStride) return HSQ_ERR_INVALID_ARG;
