@@ -42,18 +42,36 @@ class FakeTensor:
     def numel(self):
         return self.shape.numel()
 
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        s = tuple(self.shape[j + 1:].numel() for j in range(len(self.shape)))
+        return s if i is None else s[i]
+
+    address = FAR
+
     def data_ptr(self):
-        return FAR
+        return self.address
 
 
 class FakeLibrary:
     """Records every call with the device that is current during it."""
 
     def __init__(self, current):
-        self.calls, self.current = [], current
+        self.calls, self.args, self.current = [], None, current
 
     def __getattr__(self, name):
-        return lambda *a: self.calls.append((name, self.current[-1], a[-1])) or 0
+        def call(*a):
+            self.calls.append((name, self.current[-1], a[-1]))
+            self.args = a
+            return 0
+        return call
+
+    def struct(self, kind, i):
+        """Argument i of the last call, as the C structure that it points to."""
+        a = self.args[i]
+        return kind.from_buffer_copy(a if isinstance(a, bytes) else bytes(a._obj))
 
 
 @pytest.fixture
@@ -164,3 +182,17 @@ def test_a_decode_step_of_no_sequences_does_nothing():
     assert call(0, count=-1) == INVALID
     assert call(1) == INVALID
     assert call(0, cu_seqlens=A) == INVALID  # cu_seqlens of no sequence
+
+
+def _relu_x(Y, epilogue):
+    """hsq_linear_forward_x_ep on 16 x 64 fakes (its epilogue is argument -4)."""
+    names = CALLS["hsq_linear_forward_x_ep"]
+    hsq.hsq_linear_forward_x_ep(Y=Y, epilogue=epilogue, M=16, N=64, K=64, r=4, **_tensors(0, names))
+
+
+@pytest.mark.parametrize("rows,want", [(1, 1), (4, 4), (16, 16), (1 << 31, 16), ((1 << 32) + 1, 16), ((1 << 40) + 4, 16)])
+def test_mul_rows_of_any_size(rows, want, library):
+    """A row count beyond an int says the same as one of the token count: it may not come out smaller."""
+    mul = FakeTensor(0, -(-16 // rows), 64)
+    _relu_x(FakeTensor(0, 16, 64), hsq.Epilogue("relu", mul=mul, mul_rows=rows))
+    assert -(-16 // library.struct(hsq._CEpilogue, -4).mul_rows) == -(-16 // want)

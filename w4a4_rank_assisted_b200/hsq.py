@@ -330,7 +330,8 @@ class Epilogue:
         if act not in ACTIVATIONS:
             raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTIVATIONS)})")
         self._act, self._mul, self._mul_rows, self._residual = act, mul, int(mul_rows), residual
-        c = self._c = _CEpilogue(act=ACTIVATIONS[act], mul_rows=self.mul_rows)
+        # (a call has at most 2^20 tokens: a larger row count means one row)
+        c = self._c = _CEpilogue(act=ACTIVATIONS[act], mul_rows=min(self.mul_rows, 1 << 20))
         for name, t in (("mul", mul), ("residual", residual)):
             if t is None:
                 continue
