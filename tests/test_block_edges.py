@@ -196,3 +196,42 @@ def test_mul_rows_of_any_size(rows, want, library):
     mul = FakeTensor(0, -(-16 // rows), 64)
     _relu_x(FakeTensor(0, 16, 64), hsq.Epilogue("relu", mul=mul, mul_rows=rows))
     assert -(-16 // library.struct(hsq._CEpilogue, -4).mul_rows) == -(-16 // want)
+
+
+def test_an_epilogue_reads_its_tensors_where_they_are(library):
+    """A tensor whose storage was replaced (as a module's .to() and .data do) since the epilogue was made."""
+    mul, res, Y = FakeTensor(0, 16, 64), FakeTensor(0, 16, 64), FakeTensor(0, 16, 64)
+    ep = hsq.Epilogue("silu", mul=mul, residual=res)
+    _relu_x(Y, ep)
+    mul.address, res.address, res.dtype = 3 * FAR, 4 * FAR, torch.float32
+    _relu_x(Y, ep)
+    c = library.struct(hsq._CEpilogue, -4)
+    assert (c.act, c.mul, c.mul_dtype, c.mul_rows, c.mul_ld) == (4, 3 * FAR, 0, 1, 64)
+    assert (c.residual, c.residual_dtype, c.residual_ld) == (4 * FAR, 1, 64)
+    res.dtype = torch.float16
+    with pytest.raises(ValueError):
+        _relu_x(Y, ep)
+
+
+def test_a_rotation_reads_its_frequencies_where_they_are(library):
+    f = FakeTensor(0, 32, dtype=torch.float32)
+    rot = hsq.Rotation(f, [0, 1] * 16, interleaved=True, transpose=True, scale=0.5)
+    f.address = 5 * FAR
+    x, y, pos = FakeTensor(0, 3, 2, 64), FakeTensor(0, 3, 2, 64), FakeTensor(0, 3, 2, dtype=torch.int32)
+    hsq.hsq_rope(x, y, pos, rot)
+    c = library.struct(hsq._CRotation, 6)
+    assert (c.freqs, c.pairs, c.n_axes, c.interleaved, c.transpose, c.scale) == (5 * FAR, 32, 2, 1, 1, 0.5)
+    at = hsq._CRotation.pair_axis.offset
+    assert ctypes.string_at(int.from_bytes(bytes(c)[at:at + 8], "little"), 32) == bytes([0, 1] * 16)
+    f.dtype = torch.float64
+    with pytest.raises(ValueError):
+        hsq.hsq_rope(x, y, pos, rot)
+    f.dtype, f.shape = torch.float32, torch.Size((16,))
+    with pytest.raises(ValueError):
+        hsq.hsq_rope(x, y, pos, rot)
+
+
+def test_the_packed_epilogue_is_the_structure():
+    assert hsq._EPILOGUE.size == ctypes.sizeof(hsq._CEpilogue)
+    got = hsq._CEpilogue.from_buffer_copy(hsq._EPILOGUE.pack(*range(1, 9)))
+    assert [getattr(got, n) for n, _ in hsq._CEpilogue._fields_] == list(range(1, 9))

@@ -311,14 +311,18 @@ def _out_dtype(t: torch.Tensor, what: str) -> int:
     raise ValueError(f"{what} is bfloat16 or float32, not {t.dtype}")
 
 
+#: hsq_epilogue as C lays it out.
+_EPILOGUE = struct.Struct("@iPiiqPiq")
+
+
 class Epilogue:
     """What a forward does to its result before it is rounded and written:
     ``act(z) * mul + residual`` (hsq_epilogue).  ``act``: a name of ACTIVATIONS.
     ``mul``: rows of N values, token m takes row ``m // mul_rows``; ``residual``:
     M rows of N values (Y itself adds onto it in place).  Both may be column
     ranges of wider tensors (last dimension dense, row stride a multiple of 8).
-    The object keeps the tensors and is reused from call to call; what it was made
-    with is fixed."""
+    The object keeps the tensors and is reused from call to call; which tensors it
+    was made with is fixed, where they live is asked in every call."""
 
     act = property(lambda self: self._act)
     mul = property(lambda self: self._mul)
@@ -330,20 +334,20 @@ class Epilogue:
         if act not in ACTIVATIONS:
             raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTIVATIONS)})")
         self._act, self._mul, self._mul_rows, self._residual = act, mul, int(mul_rows), residual
-        # (a call has at most 2^20 tokens: a larger row count means one row)
-        c = self._c = _CEpilogue(act=ACTIVATIONS[act], mul_rows=min(self.mul_rows, 1 << 20))
-        for name, t in (("mul", mul), ("residual", residual)):
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError("libhsq takes CUDA tensors only")
-            if t.dim() != 2 or t.stride(1) != 1:
-                raise ValueError(f"{name} is a matrix with a dense last dimension")
-            setattr(c, name, t.data_ptr())
-            setattr(c, name + "_dtype", _out_dtype(t, name))
-            setattr(c, name + "_ld", t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8)
+        self._operand("mul", mul), self._operand("residual", residual)
 
-    def _for(self, Y: torch.Tensor, M: int, N: int):
+    @staticmethod
+    def _operand(name: str, t: Optional[torch.Tensor]):
+        """Address, type and row stride of an operand as it is now."""
+        if t is None:
+            return 0, 0, 0
+        if not t.is_cuda:
+            raise ValueError("libhsq takes CUDA tensors only")
+        if t.dim() != 2 or t.stride(1) != 1:
+            raise ValueError(f"{name} is a matrix with a dense last dimension")
+        return t.data_ptr(), _out_dtype(t, name), t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+    def _for(self, Y: torch.Tensor, M: int, N: int) -> bytes:
         """The C struct, once the operands' shapes and device are those of Y."""
         mul, residual = self._mul, self._residual
         if mul is not None and (self._mul_rows < 1 or tuple(mul.shape) != (-(-M // self._mul_rows), N)):
@@ -353,7 +357,10 @@ class Epilogue:
         for t in (mul, residual):
             if t is not None and t.get_device() != Y.get_device():
                 raise ValueError("the epilogue's operands live on another device than Y")
-        return ctypes.byref(self._c)
+        p, kind, ld = self._operand("mul", mul)
+        # (a call has at most 2^20 tokens: a larger row count means one row)
+        return _EPILOGUE.pack(ACTIVATIONS[self._act], p, kind, min(max(self._mul_rows, 0), 1 << 20), ld,
+                              *self._operand("residual", residual))
 
 
 def _ep(epilogue: Optional[Epilogue], Y, M, N, out, *inputs):
@@ -419,10 +426,14 @@ _CACHE_DTYPES = {**_HEAD_DTYPES, torch.float8_e4m3fn: HSQ_E4M3}
 _POS_DTYPES = {torch.int32: HSQ_POS_I32, torch.int64: HSQ_POS_I64, torch.float32: HSQ_POS_F32}
 
 
+_POINTER = struct.Struct("@P")
+
+
 class Rotation:
     """A rotation of heads by positions (hsq_rotation): ``freqs`` [pairs] fp32,
     ``pair_axes`` the axis of every pair (None: one axis).  The object keeps the
-    frequencies and is reused from call to call; what it was made with is fixed."""
+    frequencies and is reused from call to call; what it was made with is fixed (their
+    values are read on the GPU by every call, and where they live is asked in each)."""
 
     freqs = property(lambda self: self._freqs)
     pairs = property(lambda self: self._c.pairs)
@@ -441,9 +452,16 @@ class Rotation:
         if min(axes) < 0 or max(axes) >= HSQ_ROPE_MAX_AXES:
             raise ValueError(f"axes are 0 .. {HSQ_ROPE_MAX_AXES - 1}")
         self._freqs, self._n_axes, self._axes = freqs, max(axes) + 1, bytes(axes)
-        self._c = _CRotation(freqs=freqs.data_ptr(), pair_axis=self._axes, pairs=len(axes), n_axes=self._n_axes,
+        self._c = _CRotation(freqs=None, pair_axis=self._axes, pairs=len(axes), n_axes=self._n_axes,
                              interleaved=int(bool(interleaved)), transpose=int(bool(transpose)), scale=float(scale))
-        self._ref = ctypes.byref(self._c)
+        self._rest = bytes(self._c)[ctypes.sizeof(ctypes.c_void_p):]  # (holds the address of self._axes)
+
+    def _struct(self) -> bytes:
+        """The C struct, with the frequencies where they are now."""
+        f = self._freqs
+        if f.numel() != self._c.pairs or f.dtype != torch.float32 or not f.is_contiguous():
+            raise ValueError(f"freqs is no longer a contiguous float32 vector of {self._c.pairs}")
+        return _POINTER.pack(f.data_ptr()) + self._rest
 
 
 # The structures of the two calls below, packed as C lays them out: a call of a few
@@ -489,7 +507,7 @@ def _on_device(index: int, stream, call):
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
             return call(_stream(stream))
-    return call(_stream(stream))
+    return call(_raw_stream(index) if stream is None and _raw_stream is not None else _stream(stream))
 
 
 def hsq_rope(x: torch.Tensor, y: torch.Tensor, positions: torch.Tensor, rotation: Rotation, stream=None) -> None:
@@ -502,11 +520,11 @@ def hsq_rope(x: torch.Tensor, y: torch.Tensor, positions: torch.Tensor, rotation
     shape = x.shape
     hx = _heads(x, "x")
     hy = hx if y is x else _heads(y, "y", shape)
-    pos = _positions(positions, rotation)
+    pos, rot = _positions(positions, rotation), rotation._struct()
     index = x.get_device()
     _same_device(index, y, positions, rotation._freqs)
     _check(_on_device(index, stream, lambda s: load().hsq_rope(
-        hx, hy, kind, shape[0], shape[1], shape[2], rotation._ref, pos, s)), "hsq_rope")
+        hx, hy, kind, shape[0], shape[1], shape[2], rot, pos, s)), "hsq_rope")
 
 
 def hsq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -568,7 +586,7 @@ def hsq_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cac
     rot = pos = None
     index = k.get_device()
     if rotation is not None:
-        rot = rotation._ref
+        rot = rotation._struct()
         _same_device(index, rotation._freqs)
         if positions is not None:
             pos = _positions(positions, rotation)
