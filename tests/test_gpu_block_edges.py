@@ -4,7 +4,9 @@ gives, blocks that take several passes, objects that outlive what they were made
 import pytest
 import torch
 
-from test_gpu_kv_append import Batch
+from test_gpu_epilogue import SHAPES, Layer
+from test_gpu_kv_append import Batch, run_and_check
+from test_gpu_rope import angles, check, rotate64
 from w4a4_rank_assisted_b200 import hsq
 from w4a4_rank_assisted_b200.synth import LayerSpec, make_layer
 
@@ -126,3 +128,79 @@ def test_what_is_only_moved_keeps_its_bits(dtype, D, pairs, off, adjacent):
         vc = torch.zeros(4, page, kv, D, device=DEV)
         hsq.hsq_kv_append(k, v, vc.clone(), vc, table, zero, cu_seqlens=cu)
         assert torch.equal(vc[pages, slots].contiguous().view(torch.int32) >> 16, v.contiguous().view(torch.int16).int())
+
+
+# A block takes a second pass from 18 blocks per SM on (2664 on 148 SMs).  (tokens, heads, dim, pairs, adjacent): 33
+# heads of 128 are one block of a token in bf16 and two in fp32, five heads of 511 single elements' units are three,
+# whose threads walk over two units each.
+MANY = [(6001, 33, 128, 64, False), (6001, 33, 128, 64, True), (5401, 33, 128, 32, False), (1999, 5, 511, 3, True),
+        (1999, 5, 511, 3, False)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(map(str, c)))
+def test_rotation_in_several_passes(case, dtype):
+    T, H, D, P, adjacent = case
+    g = torch.Generator().manual_seed(T)
+    freqs = (100.0 ** (-torch.arange(P, dtype=torch.float64) / P)).float().to(DEV)
+    axes = torch.arange(P) % 2
+    wide = torch.randn(T, H + 1, D, generator=g).to(dtype).to(DEV)
+    x = wide[:, :H]
+    pos = torch.randint(0, 5000, (T, 2), generator=g).to(DEV)
+    rot = hsq.Rotation(freqs, axes.tolist(), interleaved=adjacent, scale=0.75)
+    y = torch.full((T, H, D), float("nan"), device=DEV, dtype=dtype)
+    hsq.hsq_rope(x, y, pos, rot)
+    want, m = rotate64(x, angles(pos, freqs, axes), adjacent, False, 0.75)
+    check(y, want, m, str(case))
+    assert torch.equal(y[..., 2 * P:], x[..., 2 * P:])
+    w = wide.clone()
+    hsq.hsq_rope(w[:, :H], w[:, :H], pos, rot)
+    assert torch.equal(w[:, :H], y) and torch.equal(w[:, H:], wide[:, H:])
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (BF, torch.float8_e4m3fn), (F32, BF), (BF, F32)],
+                         ids=["bf16", "e4m3", "f32-bf16", "bf16-f32"])
+@pytest.mark.parametrize("big", [True, False], ids=["128", "511"])
+def test_append_in_several_passes(big, dtype, cache):
+    """Ragged prompts whose tokens end inside a block's passes, padding in front and behind, an inactive sequence."""
+    q, kv, D, P, real = (32, 8, 128, 64, 6001) if big else (2, 2, 511, 3, 2101)
+    lens = [3, 77, -1, 0, 250, 16]
+    n = [real // 7, 0, real // 5, 1, real // 3]
+    n.append(real - sum(n))
+    f = (100.0 ** (-torch.arange(P, dtype=torch.float64) / P)).float().to(DEV)
+    scale = [0.02 + 0.1 * torch.rand(kv, device=DEV) for _ in range(2)] if cache == torch.float8_e4m3fn else [None, None]
+    for rot, inplace, adjacent in ((hsq.Rotation(f), False, False), (hsq.Rotation(f, interleaved=True), True, True),
+                                   (None, False, False)):
+        b = Batch(n, lens, 16, kv, q, D, dtype, cache, "heads" if inplace else "slots", pad=5, seed=real, first=2)
+        run_and_check(b, rot, f, adjacent, k_scale=scale[0], v_scale=scale[1], q_in_place=inplace)
+
+
+@pytest.mark.parametrize("i", range(len(SHAPES)), ids=lambda i: "-".join(map(str, SHAPES[i])))
+def test_an_epilogue_rounds_once_and_repeats(i):
+    """bf16 outputs are the fp32 outputs of the same call rounded once, and every repetition has the same bits."""
+    form, fmt, M, K, N, r, group = SHAPES[i]
+    lay = Layer(M, K, N, r, group, fmt, seed=i)
+    ep = hsq.Epilogue("silu", mul=torch.randn(M, N, device=DEV).to(BF), residual=torch.randn(M, N, device=DEV))
+    full, half = torch.empty(M, N, device=DEV), torch.empty(M, N, device=DEV, dtype=BF)
+    lay(form, full, ep)
+    lay(form, half, ep)
+    assert torch.equal(half, full.to(BF))
+    for Y in (full, half) * 5:
+        want = Y.clone()
+        Y.fill_(float("nan"))
+        lay(form, Y, ep)
+        assert torch.equal(Y, want)
+
+
+def test_a_long_stream_with_an_epilogue_rounds_once_and_repeats():
+    """One token, K = 4096, N = 12288: all SMs, several weight stages a block; among other launches and on its own."""
+    lay = Layer(1, 4096, 12288, 4, 64, seed=5, bias=False)
+    ep = hsq.Epilogue("silu", mul=torch.randn(1, 12288, device=DEV).to(BF))
+    full, half = torch.empty(1, 12288, device=DEV), torch.empty(1, 12288, device=DEV, dtype=BF)
+    lay("fused", full, ep)
+    for k in range(200):
+        half.fill_(float("nan"))
+        if k % 3 == 0:
+            torch.cuda.synchronize()
+        lay("fused", half, ep)
+        assert torch.equal(half, full.to(BF))
