@@ -1352,6 +1352,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         if (lane == 0) *counter = 0u;
       }
       // the accumulators already hold U L2 + b (added by the tile's first unit)
+      static_assert(!Cfg::EPI || Cfg::TMA_STORE || Cfg::SWAP, "the other stores apply no epilogue");
       if constexpr (Cfg::TMA_STORE && Cfg::EPI) {
         if (tc * BN + h * CW < args.N)
           epi_apply<CW>(args.epi, ystage + dw * 4096, tr * TILE_M + static_cast<int>(crank) * BM + q * 32, tc * BN + h * CW,

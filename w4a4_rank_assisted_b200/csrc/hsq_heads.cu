@@ -205,7 +205,7 @@ hsq_status hsq_rope(const hsq_heads* x, const hsq_heads* y, hsq_dtype dtype, int
   a.x = {x->data, x->token_stride, x->head_stride};
   a.y = {y->data, y->token_stride, y->head_stride};
   a.rot = rope_table(rot, pos);
-  a.tokens = tokens; a.heads = heads; a.dim = head_dim;
+  a.tokens = tokens; a.heads = heads;
   const uintptr_t bits = view_bits(*x, tokens, heads, es) | view_bits(*y, tokens, heads, es);
   const int v = piece_width(dtype, head_dim, rot->pairs, bits);
   a.g = rope_grid(tokens, rot->pairs / v + (in_place ? 0 : (head_dim - 2 * rot->pairs) / v), heads, rot->pairs);
@@ -326,7 +326,7 @@ hsq_status hsq_kv_append(const hsq_heads* k, const hsq_heads* v, const hsq_heads
   a.table = seqs->block_table; a.table_ld = seqs->table_ld;
   a.lens = seqs->cache_lens; a.cu = seqs->cu_seqlens;
   a.tokens = tokens; a.seqs = seqs->count;
-  a.q_heads = q_heads; a.kv_heads = kv_heads; a.dim = head_dim;
+  a.q_heads = q_heads; a.kv_heads = kv_heads;
   a.pages = cache->pages; a.page_size = cache->page_size; a.max_pages = seqs->max_pages;
   a.q_in_place = in_place ? 1 : 0;
   const int pairs = rot ? rot->pairs : 0;

@@ -39,7 +39,6 @@ constexpr int kRopeHeads = 2;
 constexpr int kRopeShared = 32768;  // shared memory of a block's tokens: their angles and cache rows
 
 enum PosType { kPosI32 = 0, kPosI64 = 1, kPosF32 = 2 };
-enum HeadType { kHeadBf16 = 0, kHeadF32 = 1, kHeadE4m3 = 2 };
 
 // A rotation and the positions it reads.
 struct RopeTable {
@@ -232,7 +231,7 @@ struct RopeArgs {
   HeadsView x, y;
   RopeTable rot;
   RopeGrid g;
-  int tokens, heads, dim;
+  int tokens, heads;
 };
 
 template <typename T, int V, bool ADJ>
@@ -331,7 +330,7 @@ struct AppendArgs {
   const int* lens;     // [seqs] tokens already cached; negative: the sequence takes no part
   const int* cu;       // [seqs + 1], or nullptr: token t is sequence t's
   long long table_ld;
-  int tokens, seqs, q_heads, kv_heads, dim;
+  int tokens, seqs, q_heads, kv_heads;
   int pages, page_size, max_pages;
   int q_in_place;
 };
