@@ -11,12 +11,16 @@
 // sample (mul_rows = the sample's tokens); either operand is bf16 or fp32.
 //
 // silu(z) = z / (1 + e^-z), and the tanh gelu 0.5 z (1 + tanh u) = z / (1 + e^-2u)
-// with u = sqrt(2/pi) (z + 0.044715 z^3): one exponential and one quotient each,
-// to a few 2^-23 relative.  The erf gelu is
+// with u = sqrt(2/pi) (z + 0.044715 z^3): one exponential and one quotient each.  The
+// relative error grows with the exponent's argument t (-z or -2u), whose fp32 rounding
+// the exponential passes on: at most (9 + 6.4 |t|) 2^-24 where t > 0, a few 2^-23
+// elsewhere (silu: 16 x 2^-23 at z = -40, 32 x 2^-23 at -80).  The erf gelu is
 //     max(z, 0) - |z|/2 erfc(|z| / sqrt 2),   erfc(w) = e^(-w^2) t Q(t), t = 1 / (1 + 0.45 w),
 // Q of degree 9 fitted to erfc(w) e^(w^2) / t over all w >= 0 for the least largest
-// relative error (3.3e-8): the complement keeps its relative accuracy for negative
-// z, where 1 + erf cancels, at two special-function instructions like the others.
+// relative error (with its coefficients in fp32: 4.7e-8 up to w = 9, where e^(-w^2)
+// leaves fp32's range, 6.4e-8 beyond); e^(-w^2) adds 2 (w^2 + 1) 2^-23 or so.  The
+// complement keeps its relative accuracy for negative z, where 1 + erf cancels, at
+// two special-function instructions like the others.
 #pragma once
 
 #include <type_traits>
