@@ -204,3 +204,41 @@ def test_a_long_stream_with_an_epilogue_rounds_once_and_repeats():
             torch.cuda.synchronize()
         lay("fused", half, ep)
         assert torch.equal(half, full.to(BF))
+
+
+@pytest.mark.parametrize("form,M,r,group", [("x", 100, 4, 64), ("codes", 300, 4, 128), ("x", 700, 32, 64), ("codes", 513, 0, 64),
+                                            ("x", 3700, 4, 128), ("x", 12, 4, 64)])
+def test_an_epilogue_with_the_weights_expanded_copy(form, M, r, group):
+    """A layer whose weights were expanded once: the bits of the forward that expands them itself."""
+    lay = Layer(M, 512, 520, r, group, seed=M)
+    Y, want = (torch.empty(M, 520, device=DEV, dtype=BF) for _ in range(2))
+    ep = hsq.Epilogue("gelu_tanh", mul=torch.randn(-(-M // 7), 520, device=DEV), mul_rows=7,
+                      residual=torch.randn(M, 520, device=DEV).to(BF))
+    lay(form, want, ep)
+    lay.pl.expand()
+    lay(form, Y, ep)
+    assert torch.equal(Y, want)
+
+
+def test_append_with_several_axes_and_no_positions():
+    """Every axis then takes the token's place: the bits of one axis."""
+    f = torch.linspace(1.0, 0.01, 32, device=DEV)
+    out = []
+    for axes in (None, [0] * 10 + [1] * 11 + [3] * 11):
+        b = Batch([9, 14], [3, 40], 16, 2, 6, 64, BF, BF, pad=2)
+        run_and_check(b, hsq.Rotation(f, axes), f)
+        out.append((b.kc, b.vc, b.q_out))
+    assert all(torch.equal(x, y) for x, y in zip(*out))
+
+
+def test_append_through_a_column_range_of_a_wider_table():
+    """Rows of the block table further apart than their entries; cached lengths and starts inside longer vectors."""
+    b = Batch([5, 30, 1], [3, 16, 40], 8, 2, 4, 64, BF, torch.float8_e4m3fn)
+    f = torch.linspace(1.0, 0.01, 32, device=DEV)
+    wide = torch.full((3, b.table.shape[1] + 6), 1 << 30, dtype=torch.int32, device=DEV)
+    wide[:, 5:-1] = b.table
+    b.table = wide[:, 5:-1]
+    long = torch.full((9,), -7, dtype=torch.int32, device=DEV)
+    long[1:4], long[5:] = b.lens_t, b.cu
+    b.lens_t, b.cu = long[1:4], long[5:]
+    run_and_check(b, hsq.Rotation(f), f)
