@@ -287,13 +287,16 @@ struct EpiRows {
 // that read them back from Tensor Memory or shared memory took longer for every
 // activation and operand.  No operand waits in registers: those loaded under a
 // condition stay live from the loop over tiles on, and the accumulators spill.
+// (The NVFP4 kernel, whose registers are not split between its warps, does spill: 716
+// bytes of stores and 1744 of loads in its instantiation with an epilogue.)
 // Bound by the activation's special-function instructions (two an element: 2 us per
 // 128 x 256 tile) and by instruction latency.  Measured with the activation step, us
-// (none / silu / mul / silu * mul / silu * mul + residual): 602 / 650 / 671 / 697 / 753 at
-// M = 8192, K = 4096, N = 12288, groups of 128; 83 / 96 / 97 / 107 / 117 at M = 4096, K =
-// 1152, N = 4608, groups of 64; NVFP4 at M = 4096, K = 4608, N = 1152: 95.8 / 98.7 / 99.6 /
-// 100.7 / 104.9.  (A pass of its own over Y and mul reads and writes 600 MB at the
-// first size: 92 us.)
+// (none / silu / mul / silu * mul / silu * mul + residual): 606 / 656 / 675 / 704 / 769 at
+// M = 8192, K = 4096, N = 12288, groups of 128 (2 % either way with the clock); 82 / 93 /
+// 95 / 104 / 115 at M = 4096, K = 1152, N = 4608, groups of 64; NVFP4 at M = 4096, K =
+// 4608, N = 1152: 95.1 / 98.5 / 99.9 / 100.8 / 104.7.  An elementwise pass over Y and mul
+// (600 MB) takes 86 us at the first size, 17 at the second, 4 at the third: on these
+// tiles the epilogue saves a rounding and a launch, and hardly any time.
 template <int CW, class Acc>
 __device__ __forceinline__ void epi_apply(const EpiArgs& e, uint8_t* stg, int y0, int n0, int M, int N, Acc&& acc) {
   const EpiOperand mul{e.mul, e.mul_ld, e.mul_rows, e.mul_f32 != 0}, res{e.res, e.res_ld, 1, e.res_f32 != 0};

@@ -13,9 +13,9 @@
 // formed its own angles and walked over the heads took twice as long.)
 //
 // Bound by memory once there are enough tokens: 20.1 us at 4608 tokens x 48 heads x 128
-// in bf16 (113 MB: 5.6 TB/s, 0.86 of the copy rate), 26.5 us at 15606 x 16 x 80 in fp32
-// (160 MB: 0.92), 43 us for the append of 9203 tokens of 32 + 8 + 8 heads x 128 (226 MB:
-// 0.8); by launch and latency below: 2.3 us for one token's rotation, 3.3 us for its
+// in bf16 (113 MB: 5.6 TB/s, 0.86 of the copy rate), 26.3 us at 15606 x 16 x 80 in fp32
+// (160 MB: 0.93), 42.5 us for the append of 9203 tokens of 32 + 8 + 8 heads x 128 (226 MB:
+// 0.81); by launch and latency below: 2.2 us for one token's rotation, 3.2 us for its
 // append (a page lookup is loads that depend on one another).
 //
 // The angle: p f_i is formed in fp64 (a product of 24-bit factors is exact there;
