@@ -349,10 +349,8 @@ def _sources_sha() -> str:
 # step's layers) from one ncu capture, keyed by workload, with the hash of the
 # CUDA sources it was captured from; any other build reports null.
 NCU_TRAFFIC = {
-    # w4a4_gemm_kernel, FLUX.1 block: 85.7 / 121.2 / 237.3 MB for qkv / MLP up / MLP down.  Captured on
-    # sources whose only difference from these is the host's choice of kernels for ranks of 17 and more:
-    # the rank-4 kernel this workload runs is the same code.
-    "flux_block_r4": ("69c28b250e6de097", 148059904.0),
+    # w4a4_gemm_kernel, FLUX.1 block: 86.3 / 122.1 / 236.3 MB for qkv / MLP up / MLP down
+    "flux_block_r4": ("55991f213707a0c1", 148219733.0),
 }
 
 
